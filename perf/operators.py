@@ -342,7 +342,7 @@ def prepare(case, seed):
               u_accept=u[:rows].contiguous(), u_sample=u[rows:].contiguous(), temp=temp)
     if own:
         import nvfp4_w4a16_mtp_amd as nv
-        st.update(nv=nv, ws=nv.verify_workspace(rows, b, v, _dev(), sampled=case["sampled"]))
+        st.update(nv=nv, ws=nv.verify_workspace(max(n), b, v, _dev(), sampled=case["sampled"]))
     return st
 
 
