@@ -477,6 +477,206 @@ int moe_layer_w4a16(const uint16_t *x_bf16, int32_t m, const nvfp4_weight *route
  */
 int moe_workspace_status(void *workspace, size_t ws_bytes, uint32_t *status, void *stream);
 
+/* ---- attention of the draft step: rotary positions and an 8-bit cache ----
+ *
+ * The steps between q|k|v and o in the draft step ([new.rs] `MtpHead::new`
+ * resolves `rope_forward`, `reshape_and_cache_flash_fp8` and
+ * `paged_decode_attn_fp8`; the pages give no formulas, so the definitions
+ * here are the library's own).
+ *
+ * Strided rows of heads (host descriptor): element d of head h of row r is
+ * data[r * row_stride + h * head_stride + d], strides in elements (a
+ * head_stride of 2 * dim reads the q halves of a gated q projection in
+ * place).  data 16-byte aligned, both strides multiples of 8, head_stride >=
+ * dim, row_stride >= 0. */
+typedef struct nvfp4_head_rows {
+    uint16_t *data;       /* bf16 */
+    int64_t row_stride, head_stride;
+    int32_t heads, dim;
+} nvfp4_head_rows;
+
+/* Rotary positions (host descriptor).  Pair i < rot_dim / 2 of a row at
+ * position p turns by the angle p * inv_freq[i] (computed in fp64, so far
+ * positions keep their phase): (x, y) -> (x cos - y sin, x sin + y cos) *
+ * mscale.  The pair is (i, i + rot_dim / 2) or, with interleaved != 0,
+ * (2i, 2i + 1); elements from rot_dim on are copied.  Scaling for long
+ * contexts is in the table and mscale.  rot_dim: a positive multiple of 16,
+ * at most the rows' dim; inv_freq: device fp64 [rot_dim / 2], 8-byte aligned,
+ * radians per position. */
+typedef struct nvfp4_rope {
+    const double *inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float mscale;
+} nvfp4_rope;
+
+/* A paged 8-bit KV cache (host descriptor, device pointers).  Codes are
+ * E4M3FN; scale byte b stands for 2^(b - 127) (0 for b = 0; 255 reads as
+ * 254), one per (page, head) and for K and V each.  V lies transposed inside
+ * its page, so that the attention's matrix operands load straight from it.
+ * codes 16-byte aligned; page_tokens 16, 32, 64 or 128; head_dim 64, 128, 192
+ * or 256; kv_heads >= 1; num_pages >= 1. */
+typedef struct nvfp4_kv8_cache {
+    uint8_t *k_codes;     /* [num_pages][kv_heads][page_tokens][head_dim] */
+    uint8_t *k_scales;    /* [num_pages][kv_heads] */
+    uint8_t *v_codes;     /* [num_pages][kv_heads][head_dim][page_tokens] */
+    uint8_t *v_scales;    /* [num_pages][kv_heads] */
+    int32_t num_pages, page_tokens, kv_heads, head_dim;
+} nvfp4_kv8_cache;
+
+/* A ragged batch over such a cache (host descriptor, device pointers, 4-byte
+ * aligned).  Sequence b owns rows [cu_rows[b], cu_rows[b + 1]) of the call's
+ * `rows` rows: the last n_b of its kv_lens[b] tokens, row i at position
+ * kv_lens[b] - n_b + i.  Token t lies in page block_table[b][t / page_tokens].
+ *   max_rows    host bound of n_b: rows of a sequence past it are not
+ *               computed.
+ *   max_kv_len  host bound of kv_lens, or 0 for max_pages * page_tokens; a
+ *               longer sequence is still handled, less evenly split.
+ * Values on the device that make no sense are bounded there: row ranges are
+ * cut to [0, rows), lengths to [0, max_pages * page_tokens]; rows at negative
+ * positions and tokens whose page id is outside [0, num_pages) are not
+ * written, not read (zero rows) and not attended to. */
+typedef struct nvfp4_kv8_seqs {
+    const int32_t *cu_rows;       /* [batch + 1] */
+    const int32_t *kv_lens;       /* [batch] */
+    const int32_t *block_table;   /* [batch][max_pages] */
+    int32_t batch, rows, max_rows, max_pages, max_kv_len;
+} nvfp4_kv8_seqs;
+
+/*
+ * rope_qk -- rotary positions of q and k rows.
+ *   q, q_out    rows before and after (the same shape; q_out may be q itself:
+ *               then only the rotated elements are written; otherwise the
+ *               two must not overlap).  NULL with q_out NULL: no q.
+ *   k, k_out    the same for k; at least one of q and k.
+ *   rows        rows of each (0 does nothing).
+ *   positions   device int32 [rows], 4-byte aligned, any values.
+ * Products and sums in fp64, one rounding to bf16.  dim % 8 == 0.  One launch.
+ */
+int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_head_rows *k,
+            const nvfp4_head_rows *k_out, int32_t rows, const int32_t *positions, const nvfp4_rope *rope,
+            void *stream);
+
+/*
+ * kv8_append -- quantises the rows' k and v into the cache at their positions.
+ *   k, v   [rows][kv_heads][head_dim] head rows.
+ * Per page and head, over the tokens of the page that this call writes: amax =
+ * max of the finite |x|; e = the smallest exponent >= -110 with amax <= 448 *
+ * 2^e.  A page that the call writes from its first token on takes e; a page it
+ * continues takes max(e, its present exponent), and when that grows the page's
+ * earlier codes are re-rounded to it.  code = E4M3 nearest to x * 2^-e (ties
+ * to even, saturating at 448; infinities saturate, NaN stays NaN).  Powers of
+ * two leave every kept value exact unless it falls among the subnormals.
+ * Writing the same rows again gives the same page.  After a shortened
+ * sequence the next call overwrites the dropped tokens.  A page written by
+ * the call must belong to one sequence only, and no page may occur twice in a
+ * sequence's written range (else its content is unspecified).  One launch.
+ */
+int kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvfp4_head_rows *k,
+               const nvfp4_head_rows *v, void *stream);
+
+/*
+ * rope_kv8_append -- rope_qk of q and k at the rows' positions in their
+ * sequences, then kv8_append of the rotated k (rounded to bf16, as rope_qk
+ * writes it) and v, in one launch: q_out and the cache are bit for bit those
+ * of the two calls.  The rotated k is not stored in bf16.  q and q_out may
+ * both be NULL.  Rows of q outside every sequence are not written.
+ */
+int rope_kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvfp4_rope *rope,
+                    const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_head_rows *k,
+                    const nvfp4_head_rows *v, void *stream);
+
+/*
+ * kv8_read -- the cache's values back in bf16 (exact: a code times a power of
+ * two) for the last n_b tokens of each sequence.
+ *   k_out, v_out   [rows][kv_heads][head_dim] head rows; one may be NULL.
+ *                  Tokens whose page id is out of range and rows at negative
+ *                  positions become zero rows; rows outside every sequence
+ *                  are left as they were.
+ * One launch.
+ */
+int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvfp4_head_rows *k_out,
+             const nvfp4_head_rows *v_out, void *stream);
+
+/*
+ * kv8_attention -- attention of the rows' q heads over the cache,
+ * out = softmax(scale * q k^T) v, q head h reading kv head h / (q_heads /
+ * kv_heads).  The row at position p sees the tokens t <= p and, with window >
+ * 0, of those the last `window` (itself included) and the first `sinks`.  Call
+ * it after the rows' own k and v are appended.
+ *   q           [rows][q_heads][head_dim] head rows; q_heads a multiple of
+ *               kv_heads.
+ *   scale       any finite factor; window, sinks >= 0 (sinks without a window
+ *               changes nothing).
+ *   out         bf16, row r head h at out + r * out_row_stride + h * head_dim
+ *               (the o projection's activation row), 16-byte aligned,
+ *               out_row_stride a multiple of 8, >= q_heads * head_dim.
+ *               A row that sees no token becomes zero; rows outside every
+ *               sequence are left as they were.
+ *   workspace   kv8_attention_workspace_bytes(cache, seqs, q_heads) bytes,
+ *               256-byte aligned, zero-filled before its first use (every call
+ *               leaves its counters at zero); one call at a time per
+ *               workspace.  The size depends only on the host fields of the
+ *               descriptors.
+ * Scores, softmax statistics and sums in fp32; weights are rounded to bf16
+ * for the product with v.  What a row does not see never reaches it, NaN
+ * included.  The result is the same on every call with the same arguments.
+ */
+size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);
+int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, float scale,
+                  int32_t window, int32_t sinks, uint16_t *out, int64_t out_row_stride, void *workspace,
+                  size_t ws_bytes, void *stream);
+
+/*
+ * verify_drafts -- which drafted tokens stand, and the token after them, from
+ * the target's logits and given random numbers (the step after [v4_mtp.rs]
+ * `propose`; `after_verify` then trims the cache).  Sequence b owns rows
+ * [cu_rows[b], cu_rows[b + 1]) of `rows` rows, n_b of them: row i holds the
+ * target's logits after i of its n_b - 1 drafts, and draft_ids[row] the draft
+ * that follows the row (not read for a sequence's last row).
+ *   logits       [rows] x vocab of logits_dtype (NVFP4_OUT_F32 or
+ *                NVFP4_OUT_BF16), row r at r * row_stride elements
+ *                (row_stride >= vocab), aligned to its element.  vocab
+ *                1..2^24.
+ *   draft_logits NULL: the drafts were chosen outright (the LM head's argmax).
+ *                Else the rows of the draft's logits, same type and stride
+ *                draft_stride: the draft of row r was sampled from row r.
+ *   max_rows     host bound of n_b, 1..64; a longer sequence is cut to it.
+ *   temperature  NULL (1), or device fp32 [batch]: divides both models'
+ *                logits; 0, below 0 or not finite means greedy.
+ *   u_accept     device fp32 [rows], u_sample device fp32 [batch]: random
+ *                numbers in [0, 1).
+ *   kv_lens      NULL, or device int32 [batch]: cache lengths with the
+ *                sequence's n_b rows appended.
+ * With p the target's softmax of a row and q the draft's (1 at the draft for
+ * outright drafts), draft d stands when u_accept * q(d) < p(d); greedily, when
+ * it is the row's first maximum.  At the first row whose draft falls, the token
+ * is drawn from max(p - q, 0), or from p after the last draft: the lowest i
+ * whose running sum exceeds u_sample times the whole (greedily: the first
+ * maximum; from p should the difference vanish everywhere).  Softmax, sums and
+ * comparisons in fp64.  A draft id outside [0, vocab) falls.  A target row
+ * without a finite sum (NaN, +inf, or nothing above -inf) is taken greedily by
+ * the scan of lmhead_gemv_argmax; such a draft row counts as an outright draft.
+ *   out_accepted [batch] int32: drafts that stand.
+ *   out_tokens   [rows] int32: the standing drafts, the drawn token, then -1.
+ *   out_next     [batch] int32: the drawn token (-1 for a sequence without
+ *                rows).
+ *   out_kv_lens  [batch] int32 (with kv_lens; may be kv_lens itself): the
+ *                lengths without the rows of fallen drafts, kv_lens - n_b +
+ *                accepted + 1.
+ *   workspace    verify_drafts_workspace_bytes(batch, max_rows, vocab,
+ *                draft_logits != NULL) bytes, 16-byte aligned; nothing to
+ *                initialise; one call at a time per workspace.
+ * int32 and fp32 arrays 4-byte aligned.  Two launches (three with
+ * draft_logits).
+ */
+size_t verify_drafts_workspace_bytes(int32_t batch, int32_t max_rows, int32_t vocab, int32_t with_draft_logits);
+int verify_drafts(const void *logits, int32_t logits_dtype, int64_t row_stride, int32_t vocab, const void *draft_logits,
+                  int64_t draft_stride, const int32_t *cu_rows, int32_t batch, int32_t rows, int32_t max_rows,
+                  const int32_t *draft_ids, const float *temperature, const float *u_accept, const float *u_sample,
+                  const int32_t *kv_lens, int32_t *out_accepted, int32_t *out_tokens, int32_t *out_next,
+                  int32_t *out_kv_lens, void *workspace, size_t ws_bytes, void *stream);
+
 /* Message of the last failing call on this host thread ("" if none); the
  * pointer stays valid until the next call on the same thread. */
 const char *nvfp4_mtp_last_error(void);

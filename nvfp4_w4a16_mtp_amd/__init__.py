@@ -22,12 +22,20 @@ Operations (same names as the C ABI):
   moe_w4a16_gemv_trace         ... one token, with per-workgroup phase timestamps
   moe_layer_w4a16              router + routed experts + gated shared expert
   moe_workspace_status         sticky status of a MoE workspace (host query)
+  rope_qk                      rotary positions of q and k rows (rope_frequencies makes the table)
+  kv8_append                   k and v rows quantised into a paged 8-bit cache (KV8Cache, KV8Seqs)
+  rope_kv8_append              ... with q and k rotated in the same launch
+  kv8_read                     the cache's values back in bf16
+  kv8_attention                attention over that cache (one token to prompt chunks, window and sinks)
+  verify_drafts                which drafted tokens stand, the token after them, the cache lengths left
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -50,6 +58,28 @@ class _MoeWeights(ctypes.Structure):
                 ("gate_codes", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p), ("gate_global", ctypes.c_void_p),
                 ("up_codes", ctypes.c_void_p), ("up_scales", ctypes.c_void_p), ("up_global", ctypes.c_void_p),
                 ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p), ("down_global", ctypes.c_void_p)]
+
+
+class _HeadRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class _KV8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KV8Seqs(ctypes.Structure):
+    _fields_ = [("cu_rows", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
 
 
 class NVFP4Error(RuntimeError):
@@ -94,13 +124,26 @@ def lib():
         L.moe_layer_w4a16_workspace_bytes.restype = sz
         L.moe_layer_w4a16.argtypes = [P, i32, WP, i32, EP, WP, WP, WP, P, P, P, P, P, P, sz, P]
         L.moe_workspace_status.argtypes = [P, sz, ctypes.POINTER(u32), P]
+        HP, RP, CP, SP = (ctypes.POINTER(t) for t in (_HeadRows, _Rope, _KV8Cache, _KV8Seqs))
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.rope_qk.argtypes = [HP, HP, HP, HP, i32, P, RP, P]
+        L.kv8_append.argtypes = [CP, SP, HP, HP, P]
+        L.rope_kv8_append.argtypes = [CP, SP, RP, HP, HP, HP, HP, P]
+        L.kv8_read.argtypes = [CP, SP, HP, HP, P]
+        L.kv8_attention_workspace_bytes.argtypes = [CP, SP, i32]
+        L.kv8_attention_workspace_bytes.restype = sz
+        L.kv8_attention.argtypes = [HP, CP, SP, f32, i32, i32, P, i64, P, sz, P]
+        L.verify_drafts_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.verify_drafts_workspace_bytes.restype = sz
+        L.verify_drafts.argtypes = [P, i32, i64, i32, P, i64, P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
         L.nvfp4_mtp_last_error.restype = ctypes.c_char_p
         for f in ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_grouped", "w4a16_gemm_m128", "lmhead_gemv_argmax",
                   "lmhead_gemv_argmax_noalloc",
                   "lmhead_gemv_argmax_logprob", "lmhead_gemv_argmax_masked", "embed_from_argmax", "lmhead_gemv_argmax_embed",
                   "lmhead_gemv_argmax_fc",
                   "w4a16_gemv_embed",
-                  "moe_w4a16_gemv", "moe_w4a16_gemv_trace", "moe_layer_w4a16", "moe_workspace_status"):
+                  "moe_w4a16_gemv", "moe_w4a16_gemv_trace", "moe_layer_w4a16", "moe_workspace_status",
+                  "rope_qk", "kv8_append", "rope_kv8_append", "kv8_read", "kv8_attention", "verify_drafts"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -603,3 +646,341 @@ def moe_layer_w4a16(x: torch.Tensor, router: NVFP4Weight, top_k: int, experts: N
                                  workspace.numel(), _stream(x)), "moe_layer_w4a16")
     return out, topk_ids, topk_w, router_logits
 
+
+
+# ---- attention of the draft step over a paged 8-bit cache, and verification
+
+@dataclass
+class KV8Cache:
+    """A paged 8-bit KV cache on the device: k_codes [pages, kv_heads,
+    page_tokens, head_dim] and v_codes [pages, kv_heads, head_dim,
+    page_tokens] uint8 (E4M3), k_scales and v_scales [pages, kv_heads] uint8
+    (byte b stands for 2^(b - 127))."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    @staticmethod
+    def empty(num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 16, device="cuda") -> "KV8Cache":
+        def u8(*shape):
+            return torch.zeros(shape, dtype=torch.uint8, device=device)
+        return KV8Cache(u8(num_pages, kv_heads, page_tokens, head_dim), u8(num_pages, kv_heads),
+                        u8(num_pages, kv_heads, head_dim, page_tokens), u8(num_pages, kv_heads))
+
+    @property
+    def kv_heads(self):
+        return self.k_codes.shape[1]
+
+    @property
+    def page_tokens(self):
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self):
+        return self.k_codes.shape[3]
+
+    def desc(self) -> _KV8Cache:
+        pages, heads, tokens, dim = self.k_codes.shape
+        for t, shape, name in ((self.k_codes, (pages, heads, tokens, dim), "k_codes"),
+                               (self.v_codes, (pages, heads, dim, tokens), "v_codes"),
+                               (self.k_scales, (pages, heads), "k_scales"), (self.v_scales, (pages, heads), "v_scales")):
+            _dev(t, name)
+            if t.dtype != torch.uint8 or t.shape != shape:
+                raise ValueError(f"{name} must be uint8 {list(shape)}")
+        _one_device(self.k_codes, k_scales=self.k_scales, v_codes=self.v_codes, v_scales=self.v_scales)
+        return _KV8Cache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                         self.v_scales.data_ptr(), pages, tokens, heads, dim)
+
+
+@dataclass
+class KV8Seqs:
+    """A ragged batch over a KV8Cache: cu_rows [batch + 1], kv_lens [batch]
+    (this call's rows included) and block_table [batch, max_pages] int32 on
+    the device; max_rows bounds a sequence's rows, max_kv_len its length (0:
+    what the table holds)."""
+    cu_rows: torch.Tensor
+    kv_lens: torch.Tensor
+    block_table: torch.Tensor
+    max_rows: int
+    max_kv_len: int = 0
+
+    def desc(self, rows: int) -> _KV8Seqs:
+        batch = self.kv_lens.numel()
+        for t, name in ((self.cu_rows, "cu_rows"), (self.kv_lens, "kv_lens"), (self.block_table, "block_table")):
+            _int32(t, name)
+        if self.cu_rows.numel() != batch + 1 or self.block_table.dim() != 2 or self.block_table.shape[0] != batch:
+            raise ValueError("need cu_rows [batch + 1], kv_lens [batch], block_table [batch][max_pages]")
+        return _KV8Seqs(self.cu_rows.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(), batch, rows,
+                        self.max_rows, self.block_table.shape[1], self.max_kv_len)
+
+
+def _int32(t: torch.Tensor, name: str):
+    _dev(t, name)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+
+
+def _one_device(first: torch.Tensor, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _rows(t: torch.Tensor, name: str) -> _HeadRows:
+    """Head rows of a bf16 [rows][heads][dim] tensor (unit stride in dim)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be bf16 [rows][heads][dim] with unit stride in dim")
+    n, heads, dim = t.shape
+    row = t.stride(0) if n > 1 else heads * dim
+    return _HeadRows(t.data_ptr(), row, t.stride(1) if heads > 1 else dim, heads, dim)
+
+
+def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, mscale: float) -> _Rope:
+    _dev(inv_freq, "inv_freq")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a float64 vector (rope_frequencies)")
+    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), mscale)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int = 4096, low_turns: float = 1.0, high_turns: float = 32.0, device="cuda"):
+    """(inv_freq, mscale) of rope_qk for `rot_dim` rotated elements:
+    f_i = base^(-2i / rot_dim), scaled for a context `factor` times
+    original_len:
+      None        as it is;
+      "linear"    f_i / factor (positions squeezed into the trained range);
+      "base"      base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is
+                  stretched by factor, the fastest not at all;
+      "by_parts"  a pair that turns more than high_turns times in original_len
+                  is kept, one below low_turns divided by factor, linear in
+                  the turns in between; mscale = 1 + 0.1 ln(factor).
+    inv_freq is float64 on `device`."""
+    if rot_dim < 16 or rot_dim % 16:
+        raise ValueError("rot_dim must be a positive multiple of 16")
+    if not base > 0 or not factor >= 1:
+        raise ValueError("need base > 0 and factor >= 1")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "base":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    f = torch.exp(-math.log(base) * i / rot_dim)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        keep = ((original_len * f / (2 * math.pi) - low_turns) / (high_turns - low_turns)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        mscale = 0.1 * math.log(factor) + 1.0
+    return f.to(device), mscale
+
+
+def rope_qk(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+            interleaved: bool = False, mscale: float = 1.0, q_out: torch.Tensor | None = None,
+            k_out: torch.Tensor | None = None):
+    """Rotary positions (int32 [rows]) of q and k, bf16 [rows][heads][dim]
+    (either may be None; rows and heads may be strided).  Returns (q_out,
+    k_out); pass q_out=q to rotate in place."""
+    _int32(positions, "positions")
+    rows = positions.numel()
+    descs, outs = [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            descs += [None, None]
+            outs.append(None)
+            continue
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if x.shape[0] != rows or out.shape != x.shape:
+            raise ValueError(f"{name} and {name}_out must have {rows} rows and one shape")
+        _one_device(positions, **{name: x, name + "_out": out})
+        descs += [ctypes.byref(_rows(x, name)), ctypes.byref(_rows(out, name + "_out"))]
+        outs.append(out)
+    _one_device(positions, inv_freq=inv_freq)
+    rp = _rope_desc(inv_freq, interleaved, mscale)
+    with torch.cuda.device(positions.device):
+        _check(lib().rope_qk(*descs, rows, _ptr(positions), ctypes.byref(rp), _stream(positions)), "rope_qk")
+    return tuple(outs)
+
+
+def kv8_append(cache: KV8Cache, seqs: KV8Seqs, k: torch.Tensor, v: torch.Tensor):
+    """Quantises k and v, bf16 [rows][kv_heads][head_dim], into the cache at
+    the rows' positions."""
+    dk, dv = _rows(k, "k"), _rows(v, "v")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape")
+    _one_device(cache.k_codes, k=k, v=v, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows, block_table=seqs.block_table)
+    c, s = cache.desc(), seqs.desc(k.shape[0])
+    with torch.cuda.device(k.device):
+        _check(lib().kv8_append(ctypes.byref(c), ctypes.byref(s), ctypes.byref(dk), ctypes.byref(dv), _stream(k)),
+               "kv8_append")
+
+
+def rope_kv8_append(cache: KV8Cache, seqs: KV8Seqs, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                    inv_freq: torch.Tensor, interleaved: bool = False, mscale: float = 1.0,
+                    q_out: torch.Tensor | None = None):
+    """rope_qk of q and k at the rows' positions, then kv8_append of the
+    rotated k and of v, in one launch.  Returns the rotated q (None without
+    q); pass q_out=q to rotate in place."""
+    dk, dv = _rows(k, "k"), _rows(v, "v")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape")
+    dq = dqo = None
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if q.shape[0] != k.shape[0] or q_out.shape != q.shape:
+            raise ValueError("q and q_out must have k's rows and one shape")
+        dq, dqo = ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(q_out, "q_out"))
+    _one_device(cache.k_codes, q=q, q_out=q_out, k=k, v=v, inv_freq=inv_freq, kv_lens=seqs.kv_lens,
+                cu_rows=seqs.cu_rows, block_table=seqs.block_table)
+    rp = _rope_desc(inv_freq, interleaved, mscale)
+    c, s = cache.desc(), seqs.desc(k.shape[0])
+    with torch.cuda.device(k.device):
+        _check(lib().rope_kv8_append(ctypes.byref(c), ctypes.byref(s), ctypes.byref(rp), dq, dqo, ctypes.byref(dk),
+                                     ctypes.byref(dv), _stream(k)), "rope_kv8_append")
+    return q_out
+
+
+def kv8_read(cache: KV8Cache, seqs: KV8Seqs, rows: int | None = None, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None):
+    """The values of each sequence's last tokens (as many as it owns rows) in
+    bf16 [rows][kv_heads][head_dim].  Give the outputs, or `rows` to have both
+    allocated here.  Returns (k_out, v_out)."""
+    if k_out is None and v_out is None:
+        if rows is None:
+            raise ValueError("kv8_read needs rows, k_out or v_out")
+        shape = (rows, cache.kv_heads, cache.head_dim)
+        k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device) for _ in range(2))
+    some = k_out if k_out is not None else v_out
+    if rows is None:
+        rows = some.shape[0]
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and t.shape[0] != rows:
+            raise ValueError(f"{name} must have {rows} rows")
+    _one_device(cache.k_codes, k_out=k_out, v_out=v_out, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows,
+                block_table=seqs.block_table)
+    dk = ctypes.byref(_rows(k_out, "k_out")) if k_out is not None else None
+    dv = ctypes.byref(_rows(v_out, "v_out")) if v_out is not None else None
+    c, s = cache.desc(), seqs.desc(rows)
+    with torch.cuda.device(some.device):
+        _check(lib().kv8_read(ctypes.byref(c), ctypes.byref(s), dk, dv, _stream(some)), "kv8_read")
+    return k_out, v_out
+
+
+def kv8_attention_workspace(cache: KV8Cache, seqs: KV8Seqs, q_heads: int, rows: int) -> torch.Tensor:
+    """Zero-filled workspace for kv8_attention of `rows` rows (must start
+    zeroed; every call leaves it reusable)."""
+    c, s = cache.desc(), seqs.desc(rows)
+    with torch.cuda.device(cache.k_codes.device):
+        nbytes = lib().kv8_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(s), q_heads)
+    if nbytes == 0:
+        raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
+    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float | None = None, window: int = 0,
+                  sinks: int = 0, workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Attention of q, bf16 [rows][q_heads][head_dim], over the cache (scale:
+    head_dim^-0.5 by default).  out: bf16 [rows][q_heads][head_dim], heads
+    contiguous."""
+    dq = _rows(q, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    do = _rows(out, "out")
+    if out.shape != q.shape or do.head_stride != q.shape[2]:
+        raise ValueError("out must have q's shape and contiguous heads")
+    if workspace is None:
+        workspace = kv8_attention_workspace(cache, seqs, q.shape[1], q.shape[0])
+    _dev(workspace, "workspace")
+    _one_device(cache.k_codes, q=q, out=out, workspace=workspace, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows,
+                block_table=seqs.block_table)
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    c, s = cache.desc(), seqs.desc(q.shape[0])
+    with torch.cuda.device(q.device):
+        _check(lib().kv8_attention(ctypes.byref(dq), ctypes.byref(c), ctypes.byref(s), scale, window, sinks, _ptr(out),
+                                   do.row_stride, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                   _stream(q)), "kv8_attention")
+    return out
+
+
+class Verified(NamedTuple):
+    """accepted [batch]: drafts that stand; tokens [rows]: those, the token
+    drawn after them, then -1; next [batch]: the drawn token; kv_lens [batch]:
+    cache lengths without the fallen drafts' rows (None if not asked for)."""
+    accepted: torch.Tensor
+    tokens: torch.Tensor
+    next: torch.Tensor
+    kv_lens: torch.Tensor | None
+
+
+def verify_workspace(max_rows: int, batch: int, vocab: int, device, sampled: bool = False) -> torch.Tensor:
+    """Workspace for verify_drafts (nothing to initialise)."""
+    with torch.cuda.device(device):
+        nbytes = lib().verify_drafts_workspace_bytes(batch, max_rows, vocab, int(sampled))
+    if nbytes == 0:
+        raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def verify_drafts(logits: torch.Tensor, cu_rows: torch.Tensor, draft_ids: torch.Tensor, u_accept: torch.Tensor,
+                  u_sample: torch.Tensor, max_rows: int, temperature: torch.Tensor | None = None,
+                  draft_logits: torch.Tensor | None = None, kv_lens: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, out: Verified | None = None) -> Verified:
+    """Verification of drafted tokens against the target's logits [rows][vocab]
+    (fp32 or bf16, rows may be strided), from given random numbers.  Sequence b
+    owns rows cu_rows[b] .. cu_rows[b + 1]; draft_ids[r] is the draft after row
+    r (a sequence's last row has none).  draft_logits: the rows the drafts were
+    sampled from, or None for drafts chosen outright."""
+    rows, vocab = logits.shape
+    batch = cu_rows.numel() - 1
+    for t, name in ((cu_rows, "cu_rows"), (draft_ids, "draft_ids"), (kv_lens, "kv_lens")):
+        if t is not None:
+            _int32(t, name)
+    for t, name, n in ((u_accept, "u_accept", rows), (u_sample, "u_sample", batch), (temperature, "temperature", batch)):
+        if t is None:
+            continue
+        _dev(t, name)
+        if t.dtype != torch.float32 or t.numel() != n:
+            raise ValueError(f"{name} must be float32 with {n} elements")
+    if draft_ids.numel() != rows or (kv_lens is not None and kv_lens.numel() != batch):
+        raise ValueError("need draft_ids [rows] and kv_lens [batch]")
+    for t, name in ((logits, "logits"), (draft_logits, "draft_logits")):
+        if t is not None and (not t.is_cuda or t.dtype != logits.dtype or t.shape != logits.shape or
+                              (t.stride(1) != 1 and vocab != 1)):
+            raise ValueError(f"{name} must be a device tensor of the logits' type and shape, unit column stride")
+    dev = logits.device
+    if workspace is None:
+        workspace = verify_workspace(max_rows, batch, vocab, dev, sampled=draft_logits is not None)
+    _dev(workspace, "workspace")
+    if out is None:
+        out = Verified(torch.empty(batch, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.int32, device=dev),
+                       torch.empty(batch, dtype=torch.int32, device=dev),
+                       torch.empty(batch, dtype=torch.int32, device=dev) if kv_lens is not None else None)
+    for t, name, n in ((out.accepted, "accepted", batch), (out.tokens, "tokens", rows), (out.next, "next", batch),
+                       (out.kv_lens, "kv_lens", batch)):
+        if t is not None:
+            _int32(t, "out." + name)
+            if t.numel() != n:
+                raise ValueError(f"out.{name} must have {n} elements")
+    _one_device(logits, cu_rows=cu_rows, draft_ids=draft_ids, u_accept=u_accept, u_sample=u_sample,
+                temperature=temperature, draft_logits=draft_logits, kv_lens=kv_lens, workspace=workspace,
+                accepted=out.accepted, tokens=out.tokens, next=out.next, out_kv_lens=out.kv_lens)
+
+    def stride(t):
+        return 0 if t is None else (t.stride(0) if rows > 1 else vocab)
+    with torch.cuda.device(dev):
+        _check(lib().verify_drafts(_ptr(logits), _out_code(logits.dtype), stride(logits), vocab, _ptr(draft_logits),
+                                   stride(draft_logits), _ptr(cu_rows), batch, rows, max_rows, _ptr(draft_ids),
+                                   _ptr(temperature), _ptr(u_accept), _ptr(u_sample), _ptr(kv_lens), _ptr(out.accepted),
+                                   _ptr(out.tokens), _ptr(out.next), _ptr(out.kv_lens), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(logits)), "verify_drafts")
+    return out
