@@ -511,8 +511,8 @@ typedef struct nvfp4_rope {
 } nvfp4_rope;
 
 /* A paged 8-bit KV cache (host descriptor, device pointers).  Codes are
- * E4M3FN; scale byte b stands for 2^(b - 127) (0 for b = 0; 255 reads as
- * 254), one per (page, head) and for K and V each.  V lies transposed inside
+ * E4M3FN; scale byte b stands for 2^(b - 127) (255 reads as 254), one per
+ * (page, head) and for K and V each; kv8_append writes bytes of 17 or more.  V lies transposed inside
  * its page, so that the attention's matrix operands load straight from it.
  * codes 16-byte aligned; page_tokens 16, 32, 64 or 128; head_dim 64, 128, 192
  * or 256; kv_heads >= 1; num_pages >= 1. */
@@ -587,8 +587,8 @@ int rope_kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, co
                     const nvfp4_head_rows *v, void *stream);
 
 /*
- * kv8_read -- the cache's values back in bf16 (exact: a code times a power of
- * two) for the last n_b tokens of each sequence.
+ * kv8_read -- the cache's values back in bf16 (a code times a power of two:
+ * exact for scale bytes of 17 to 246) for the last n_b tokens of each sequence.
  *   k_out, v_out   [rows][kv_heads][head_dim] head rows; one may be NULL.
  *                  Tokens whose page id is out of range and rows at negative
  *                  positions become zero rows; rows outside every sequence
@@ -619,7 +619,7 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  *               workspace.  The size depends only on the host fields of the
  *               descriptors.
  * Scores, softmax statistics and sums in fp32; weights are rounded to bf16
- * for the product with v.  What a row does not see never reaches it, NaN
+ * for the product with v and for their sum.  What a row does not see never reaches it, NaN
  * included.  The result is the same on every call with the same arguments.
  */
 size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);

@@ -39,10 +39,9 @@ __device__ __forceinline__ Seq load_seq(const Seqs &s, int b, int lp) {
     return q;
 }
 
-// Scale byte -> exponent of its power of two (255 reads as 254; byte 0 stands
-// for 0, an exponent that takes every code to 0).
-__device__ __forceinline__ int kv8_exp(uint32_t b) { return b ? (int)min(b, 254u) - 127 : -1000; }
-// ... -> its value (0 for byte 0).
+// Scale byte -> exponent of its power of two (255 reads as 254).
+__device__ __forceinline__ int kv8_exp(uint32_t b) { return (int)min(b, 254u) - 127; }
+// ... -> a float with that exponent field, the scale operand of a conversion.
 __device__ __forceinline__ float kv8_scale(uint32_t b) { return __uint_as_float(min(b, 254u) << 23); }
 
 inline HeadRows view(const nvfp4_head_rows *r) {

@@ -46,7 +46,7 @@ def scale_exp(amax):
 
 
 def scale_of(byte):
-    return 0.0 if byte == 0 else 2.0 ** (min(int(byte), 254) - 127)
+    return 2.0 ** (min(int(byte), 254) - 127)
 
 
 class Cache:
@@ -96,7 +96,7 @@ class Cache:
                         e = scale_exp(fin.max() if fin.size else 0.0)
                         if o0 > 0:
                             s = scale_of(scales[page, h])
-                            e = max(e, int(min(scales[page, h], 254)) - 127 if s else -10 ** 6)
+                            e = max(e, int(min(scales[page, h], 254)) - 127)
                             if s != 2.0 ** e:
                                 old = codes[page, h, :o0]
                                 re = e4m3_encode(E4M3[old] * (s / 2.0 ** e))
