@@ -614,13 +614,13 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  *               A row that sees no token becomes zero; rows outside every
  *               sequence are left as they were.
  *   workspace   kv8_attention_workspace_bytes(cache, seqs, q_heads) bytes,
- *               256-byte aligned, zero-filled before its first use (every call
- *               leaves its counters at zero); one call at a time per
- *               workspace.  The size depends only on the host fields of the
- *               descriptors.
+ *               256-byte aligned; nothing to initialise; one call at a time
+ *               per workspace.  The size depends only on the host fields of
+ *               the descriptors.
  * Scores, softmax statistics and sums in fp32; weights are rounded to bf16
  * for the product with v and for their sum.  What a row does not see never reaches it, NaN
- * included.  The result is the same on every call with the same arguments.
+ * included.  The result is the same on every call with the same arguments on
+ * the same device.  One or two launches.
  */
 size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);
 int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, float scale,

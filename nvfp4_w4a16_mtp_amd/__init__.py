@@ -876,14 +876,13 @@ def kv8_read(cache: KV8Cache, seqs: KV8Seqs, rows: int | None = None, k_out: tor
 
 
 def kv8_attention_workspace(cache: KV8Cache, seqs: KV8Seqs, q_heads: int, rows: int) -> torch.Tensor:
-    """Zero-filled workspace for kv8_attention of `rows` rows (must start
-    zeroed; every call leaves it reusable)."""
+    """Workspace for kv8_attention of `rows` rows (nothing to initialise)."""
     c, s = cache.desc(), seqs.desc(rows)
     with torch.cuda.device(cache.k_codes.device):
         nbytes = lib().kv8_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(s), q_heads)
     if nbytes == 0:
         raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
-    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.k_codes.device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.k_codes.device)
 
 
 def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float | None = None, window: int = 0,

@@ -37,6 +37,23 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 constexpr int kStep = 128;        // tokens a step
 constexpr float kSlack = 6.0f;
 
+// x / d for 0 <= x < 2^31 by a multiplication with a host-made reciprocal: with l =
+// ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1 and t the high word of m x, the
+// quotient is (t + (x - t) / 2) >> (l - 1).
+struct FastDiv {
+    uint32_t d, mul, sh;
+    __device__ __forceinline__ int div(int x) const {
+        if (sh == 0) return x;                        // d = 1
+        const uint32_t t = __umulhi(mul, (uint32_t)x);
+        return (int)((t + (((uint32_t)x - t) >> 1)) >> (sh - 1));
+    }
+};
+static FastDiv fast_div(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return FastDiv{d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+
 struct AttnArgs {
     HeadRows q;
     KV8 c;
@@ -46,11 +63,15 @@ struct AttnArgs {
     int window, sinks;
     uint16_t *out;
     int64_t out_stride;
-    int group;              // q heads per kv head
+    FastDiv group;          // q heads per kv head
     int row_tiles;          // row tiles of a sequence at most
-    int splits;             // pieces of the key range
-    float *part;            // partial results (splits > 1)
+    int splits;             // pieces of a row tile's keys (uneven grid)
+    int32_t *before;        // [kMaxShared + 1] steps of the sequences before b, for k_attn_join
+    float *part;            // partial results, two slots of RT row tiles a workgroup
 };
+
+// A value that is the same in every lane, into a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Maximum and sum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float v) {
@@ -134,31 +155,155 @@ struct Shared {
     int flag[2][4];
 };
 
-// One workgroup: 16 * RT rows of one (sequence, kv head), one piece of their
-// keys.
-template <int D, int RT>
+// Steps of sequence b when one row tile holds its rows: at least one if it has
+// rows (a row that sees nothing is still written), and kSetup for what a workgroup
+// spends before its first step (the loads of ids, Q, K and V in turn).
+constexpr int kSetup = 2;
+__device__ __forceinline__ int seq_steps(const AttnArgs &a, const Seq &sq) {
+    const int rows = min(sq.n, a.s.max_rows) * (int)a.group.d;
+    if (rows == 0) return 0;
+    const int shift = sq.len - sq.n;
+    return max(key_range(shift, shift + a.group.div(rows - 1), a.window, a.sinks).count, 1) + kSetup;
+}
+
+constexpr int kMaxShared = 1024;   // sequences of a batch in even shares at most
+
+// Prefix sums of the sequences' steps into before[0 .. batch] (LDS).
+__device__ __forceinline__ void count_steps(const AttnArgs &a, int *before, int *waves) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int base = 0;
+    if (tid == 0) before[0] = 0;
+    for (int b0 = 0; b0 < a.s.batch; b0 += 256) {
+        const int b = b0 + tid;
+        int run = b < a.s.batch ? seq_steps(a, load_seq(a.s, b, a.c.lp)) : 0;
+        const int n = min(a.s.batch - b0, 64);
+        for (int d = 1; d < n; d <<= 1) {
+            const int o = __shfl_up(run, d, 64);
+            if (lane >= d) run += o;
+        }
+        if (b0 + 64 < a.s.batch) {                    // more than one wavefront's sequences
+            if (lane == 63) waves[wave] = run;
+            __syncthreads();
+            for (int i = 0; i < wave; ++i) run += waves[i];
+        }
+        if (b < a.s.batch) before[b + 1] = base + run;
+        if (b0 + 256 < a.s.batch) {
+            base += waves[0] + waves[1] + waves[2] + waves[3];
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+}
+
+// Pieces in consecutive workgroups first .. first + count - 1; piece k is in slot
+// 0 of its workgroup except, perhaps, the first.
+struct Pieces {
+    int first, count, first_slot;
+    __device__ __forceinline__ int at(int k) const { return (first + k) * 2 + (k == 0 ? first_slot : 0); }
+};
+
+// Even shares of `total` steps: the first total % shares workgroups have one
+// more.
+struct Shares {
+    int q, rem;
+    __device__ __forceinline__ Shares(int total, int grid) {
+        const int shares = max(min(grid, total), 1);  // none of them empty
+        q = total / shares;
+        rem = total - q * shares;
+    }
+    __device__ __forceinline__ int begin(int i) const { return i * q + min(i, rem); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int big = rem * (q + 1);
+        return u < big ? u / (q + 1) : rem + (u - big) / q;
+    }
+    // of a pair whose n steps begin at u
+    __device__ __forceinline__ Pieces pieces(int u, int n) const {
+        const int first = owner(u);
+        return Pieces{first, owner(u + n - 1) - first + 1, begin(first) < u ? 1 : 0};
+    }
+};
+
+// One workgroup: a share of the steps.  EVEN: the steps of all (sequence, kv head)
+// pairs in order are cut into equal shares, so that every workgroup reads the same
+// number of keys however ragged the batch is (one row tile a sequence).  Else: 16 *
+// RT rows of one pair and one of `splits` pieces of their keys.  Where a pair's (a
+// row tile's) keys are spread over workgroups, each leaves a partial result in the
+// workspace, and k_attn_join adds them up in piece order.  (Joined by the last
+// workgroup to arrive instead, through device-scope accesses: 114 against 111 us for
+// one row each of 32 sequences, 102 against 80 us with 3 to 6 rows of 16.)
+template <int D, int RT, bool EVEN>
 __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 128) : 2)) void k_attn(AttnArgs a) {
     constexpr int C = D / 64, DW = D / 64;            // 64-element chunks; 16-dim tiles of a wavefront
     __shared__ Shared<D, RT> sh;
-    const int split = blockIdx.x % a.splits;
-    int w = blockIdx.x / a.splits;
-    const int rtile = a.row_tiles - 1 - w % a.row_tiles;   // the longest key ranges first
-    w /= a.row_tiles;
-    const int h = w % a.c.heads, b = w / a.c.heads;
-    const Seq sq = load_seq(a.s, b, a.c.lp);
-    const int rows = min(sq.n, a.s.max_rows) * a.group, row0 = rtile * 16 * RT;
-    if (row0 >= rows) return;
+    __shared__ int before[EVEN ? kMaxShared + 1 : 1], wave_sum[4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
-    const int shift = sq.len - sq.n;
-    const int pos_lo = shift + row0 / a.group, pos_hi = shift + (min(row0 + 16 * RT, rows) - 1) / a.group;
-    const Keys keys = key_range(pos_lo, pos_hi, a.window, a.sinks);
-    const int last_page = max(keys.end - 1, 0) >> a.c.lp;
-    const int per = (keys.count + a.splits - 1) / a.splits;
-    const int v0 = split * per, v1 = min(v0 + per, keys.count);
-    const int32_t *table = a.s.table + (int64_t)b * a.s.max_pages;
     const int64_t page_bytes = (int64_t)D << a.c.lp;
     const int pmask = (1 << a.c.lp) - 1;
+
+    int u = 0, u1 = 1;
+    Shares share(1, 1);
+    if (EVEN) {
+        count_steps(a, before, wave_sum);
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i <= a.s.batch; i += 256) a.before[i] = before[i];
+        const int total = uniform(before[a.s.batch]) * a.c.heads;
+        if ((int)blockIdx.x >= total) return;
+        share = Shares(total, gridDim.x);
+        u = share.begin(blockIdx.x);
+        u1 = share.begin(blockIdx.x + 1);
+    }
+    do {
+    int b, h, rtile, v0, v1, slot;
+    Pieces pieces;
+    Seq sq;
+    if (!EVEN) {
+        const int split = blockIdx.x % a.splits;
+        int w = blockIdx.x / a.splits;
+        rtile = a.row_tiles - 1 - w % a.row_tiles;    // the longest key ranges first
+        w /= a.row_tiles;
+        h = w % a.c.heads;
+        b = w / a.c.heads;
+        sq = load_seq(a.s, b, a.c.lp);
+        pieces = Pieces{(int)blockIdx.x - split, a.splits, 0};
+        slot = 0;
+        v0 = split;                                   // the piece; its steps follow below
+        v1 = 0;
+        u = u1;
+    } else {
+        int lo = 0, hi = a.s.batch;                   // before[lo] * heads <= u < before[hi] * heads
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (uniform(before[mid]) * a.c.heads <= u) lo = mid; else hi = mid;
+        }
+        b = lo;
+        sq = load_seq(a.s, b, a.c.lp);
+        const int steps = uniform(before[b + 1]) - uniform(before[b]), in = u - uniform(before[b]) * a.c.heads;
+        h = in / steps;
+        rtile = 0;
+        v0 = in - h * steps;
+        v1 = min(steps, v0 + (u1 - u));
+        pieces = share.pieces(u - v0 + kSetup, steps - kSetup);
+        u += v1 - v0;
+        v0 = max(v0 - kSetup, 0);
+        v1 -= kSetup;
+        if (v1 <= v0) continue;                       // the setup alone: the next workgroup has the first step
+        slot = v0 == 0 ? pieces.first_slot : 0;
+    }
+    sq = Seq{uniform(sq.r0), uniform(sq.n), uniform(sq.len)};
+    const int rows = min(sq.n, a.s.max_rows) * (int)a.group.d, row0 = rtile * 16 * RT;
+    if (!EVEN && row0 >= rows) return;
+    const int shift = sq.len - sq.n;
+    const int pos_lo = shift + a.group.div(row0), pos_hi = shift + a.group.div(min(row0 + 16 * RT, rows) - 1);
+    const Keys keys = key_range(pos_lo, pos_hi, a.window, a.sinks);
+    if (!EVEN) {
+        const int per = (keys.count + a.splits - 1) / a.splits;
+        v0 *= per;
+        v1 = v0 + per;
+    }
+    v1 = min(v1, keys.count);
+    const int last_page = max(keys.end - 1, 0) >> a.c.lp;
+    const int32_t *table = a.s.table + (int64_t)b * a.s.max_pages;
 
     auto valid = [&](int id) { return id >= 0 && id < a.c.pages; };
     // ids of the pages of the wavefront's two K blocks and of the lane's two V blocks
@@ -180,9 +325,9 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int64_t at = (int64_t)(valid(id.k[j]) ? id.k[j] : 0) * a.c.heads + h;
-            const uint8_t *p = a.c.k + at * page_bytes + (((32 * wave + 16 * j) & pmask) + r) * D + 16 * g;
+            const uint8_t *p = a.c.k + at * page_bytes + ((32 * wave + 16 * j) & pmask) * D;
 #pragma unroll
-            for (int c = 0; c < C; ++c) kf[j][c] = *reinterpret_cast<const uint4 *>(p + c * 64);
+            for (int c = 0; c < C; ++c) kf[j][c] = *reinterpret_cast<const uint4 *>(p + r * D + 16 * g + c * 64);
             sk[j] = a.c.ks[at];
         }
     };
@@ -201,31 +346,48 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
     f32x4 o[RT][DW];
     float m[RT], l[RT];
     uint32_t poison[RT];              // bit 4 dt + i: o[rt][dt][i] is NaN
+    int step = 0, next = 0;
+    Ids id{}, nid{};
+    if (v0 < v1) {
+        step = keys.step(v0);
+        id = load_ids(step);
+        next = keys.step(min(v0 + 1, v1 - 1));
+        nid = load_ids(next);
+    }
+    // Q into LDS (each wavefront a part); a scale below zero is its magnitude on the
+    // negated q
+    constexpr int QN = (RT * C * 2 + 3) / 4;
+    uint4 qv[QN];
+#pragma unroll
+    for (int k = 0; k < QN; ++k) {
+        const int f = k * 4 + wave, rt = f / (C * 2), ce = f % (C * 2);
+        const int row = min(row0 + min(rt, RT - 1) * 16 + r, rows - 1), i = a.group.div(row);
+        qv[k] = *reinterpret_cast<const uint4 *>(a.q.data + (int64_t)(sq.r0 + i) * a.q.row +
+                                                 (int64_t)(h * (int)a.group.d + row - i * (int)a.group.d) * a.q.head + 16 * g +
+                                                 32 * ce - 24 * (ce & 1));
+    }
+    if (v0 < v1) {
+        load_k(step, id);
+        load_v(step, id);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = min(row0 + rt * 16 + r, rows - 1);
-        const int i = row / a.group;
-        pos[rt] = shift + i;
+        pos[rt] = shift + a.group.div(min(row0 + rt * 16 + r, rows - 1));
         m[rt] = -INFINITY;
         l[rt] = 0.0f;
         poison[rt] = 0u;
-        const uint16_t *src = a.q.data + (int64_t)(sq.r0 + i) * a.q.row + (int64_t)(h * a.group + row % a.group) * a.q.head + 16 * g;
-        // a scale below zero is its magnitude on the negated q
-        const uint32_t flip = a.negate ? 0x80008000u : 0u;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (((rt * C + c) & 3) == wave)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint4 v = *reinterpret_cast<const uint4 *>(src + 64 * c + 8 * e);
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
-                    sh.q[rt][c][e][lane] = __builtin_bit_cast(bf16x8, v);
-                }
 #pragma unroll
         for (int dt = 0; dt < DW; ++dt) o[rt][dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (EVEN) __syncthreads();                        // the previous piece's reads of sh are over
+#pragma unroll
+    for (int k = 0; k < QN; ++k) {
+        const int f = k * 4 + wave;
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        if (f < RT * C * 2)
+            (&sh.q[0][0][0][0])[f * 64 + lane] =
+                __builtin_bit_cast(bf16x8, make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip));
     }
     __syncthreads();
 
@@ -258,13 +420,7 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
         }
     };
 
-    if (v0 < v1) {
-        int step = keys.step(v0);
-        Ids id = load_ids(step);
-        load_k(step, id);
-        load_v(step, id);
-        int next = keys.step(min(v0 + 1, v1 - 1));
-        Ids nid = load_ids(next);
+    {
         for (int v = v0; v < v1; ++v) {
             const int buf = (v - v0) & 1, cur = step;
             const bool kv_ok = __all(valid(id.k[0]) && valid(id.k[1]) && valid(id.v[0]) && valid(id.v[1]));
@@ -312,11 +468,15 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
                 mx[rt] = row_max(s, rt);
                 need |= mx[rt] > m[rt] + kSlack;
             }
-            need = __any(need);
-            write_p(buf, s, sum);
-            if (lane == 0) sh.flag[buf][wave] = need;
-            __syncthreads();
-            if (sh.flag[buf][0] | sh.flag[buf][1] | sh.flag[buf][2] | sh.flag[buf][3]) {
+            bool move = v == v0;                      // no reference yet
+            if (!move) {
+                need = __any(need);
+                write_p(buf, s, sum);
+                if (lane == 0) sh.flag[buf][wave] = need;
+                __syncthreads();
+                move = sh.flag[buf][0] | sh.flag[buf][1] | sh.flag[buf][2] | sh.flag[buf][3];
+            }
+            if (move) {
                 // move the reference to the present maximum, in every wavefront alike
                 if (lane < 16)
 #pragma unroll
@@ -415,68 +575,104 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
     __syncthreads();
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += sh.m[k][rt * 16 + r];
+        l[rt] = (sh.m[0][rt * 16 + r] + sh.m[1][rt * 16 + r]) + (sh.m[2][rt * 16 + r] + sh.m[3][rt * 16 + r]);
 #pragma unroll
         for (int dt = 0; dt < DW; ++dt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (poison[rt] >> (4 * dt + i) & 1u) o[rt][dt][i] = NAN;
-        if (a.splits > 1) {
-            float *part = a.part + (((((int64_t)b * a.c.heads + h) * a.row_tiles + rtile) * RT + rt) * a.splits + split) * part_floats<D>();
+    }
+    auto part_at = [&](int at, int rt) { return a.part + ((int64_t)at * RT + rt) * part_floats<D>(); };
+    if (pieces.count > 1) {                           // k_attn_join does the rest
 #pragma unroll
-            for (int dt = 0; dt < DW; ++dt) *reinterpret_cast<f32x4 *>(part + (wave * DW + dt) * 256 + lane * 4) = o[rt][dt];
-            if (threadIdx.x < 16) {
-                part[16 * D + r] = m[rt];
-                part[16 * D + 16 + r] = sum;
-            }
-        } else {
-            const int row = row0 + rt * 16 + r, i = row / a.group, hq = h * a.group + row % a.group;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            if (row < rows) {
-                uint16_t *dst = a.out + (int64_t)(sq.r0 + i) * a.out_stride + (int64_t)hq * D + wave * DW * 16 + 4 * g;
+        for (int rt = 0; rt < RT; ++rt) {
+            if (row0 + rt * 16 + r >= rows) continue;
+            float *p = part_at(blockIdx.x * 2 + slot, rt);
 #pragma unroll
-                for (int dt = 0; dt < DW; ++dt) store_out(dst + dt * 16, o[rt][dt] * inv);
-            }
+            for (int dt = 0; dt < DW; ++dt) *reinterpret_cast<f32x4 *>(p + (wave * DW + dt) * 256 + lane * 4) = o[rt][dt];
+            if (threadIdx.x < 16) *reinterpret_cast<float2 *>(p + 16 * D + 2 * r) = make_float2(m[rt], l[rt]);
+        }
+        continue;
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = row0 + rt * 16 + r, i = a.group.div(min(row, rows - 1)), hq = h * (int)a.group.d + row - i * (int)a.group.d;
+        const float inv = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
+        if (row < rows) {
+            uint16_t *dst = a.out + (int64_t)(sq.r0 + i) * a.out_stride + (int64_t)hq * D + wave * DW * 16 + 4 * g;
+#pragma unroll
+            for (int dt = 0; dt < DW; ++dt) store_out(dst + dt * 16, o[rt][dt] * inv);
         }
     }
+    } while (EVEN && u < u1);
 }
 
 // Joins the pieces of 16 rows: one wavefront per 16 dims.
-template <int D>
-__global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int sub_tiles) {
+template <int D, int RT, bool EVEN>
+__global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int grid) {
     const int dt = blockIdx.x % (D / 16), lane = threadIdx.x, r = lane & 15;
-    int w = blockIdx.x / (D / 16);
-    const int st = w % sub_tiles;
-    const int unit = w / sub_tiles, h = unit % a.c.heads, b = unit / a.c.heads;
+    const int w = blockIdx.x / (D / 16), rt = w % RT, tile = w / RT;
+    const int unit = tile / a.row_tiles, h = unit % a.c.heads, b = unit / a.c.heads;
     const Seq sq = load_seq(a.s, b, a.c.lp);
-    const int rows = min(sq.n, a.s.max_rows) * a.group;
-    if (st * 16 >= rows) return;
-    const float *part = a.part + (int64_t)w * a.splits * part_floats<D>();
-    float mx = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, part[(int64_t)s * part_floats<D>() + 16 * D + r]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < a.splits; ++s) {
-        const float *p = part + (int64_t)s * part_floats<D>();
-        const float f = __builtin_amdgcn_exp2f(p[16 * D + r] - ref);
-        sum += p[16 * D + 16 + r] * f;
-        o += *reinterpret_cast<const f32x4 *>(p + dt * 256 + lane * 4) * f;
+    Pieces pieces{tile * a.splits, a.splits, 0};
+    if (EVEN) {
+        const int b0 = a.before[b], steps = a.before[b + 1] - b0, total = a.before[a.s.batch] * a.c.heads;
+        if (steps == 0) return;
+        pieces = Shares(total, grid).pieces(b0 * a.c.heads + h * steps + kSetup, steps - kSetup);
+        if (pieces.count == 1) return;                // written by its workgroup
     }
-    const int row = st * 16 + r;
+    const int rows = min(sq.n, a.s.max_rows) * (int)a.group.d;
+    const int row = ((a.row_tiles - 1 - tile % a.row_tiles) * RT + rt) * 16 + r;
     if (row >= rows) return;
-    const int i = row / a.group, hq = h * a.group + row % a.group;
+    constexpr int N = 8;                              // pieces whose loads are in flight together
+    float mx = -INFINITY, sum = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < pieces.count; k0 += N) {
+        float2 ml[N];
+        f32x4 v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float *p = a.part + ((int64_t)pieces.at(min(k0 + k, pieces.count - 1)) * RT + rt) * part_floats<D>();
+            ml[k] = *reinterpret_cast<const float2 *>(p + 16 * D + 2 * r);
+            v[k] = *reinterpret_cast<const f32x4 *>(p + dt * 256 + lane * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (k0 + k >= pieces.count) continue;
+            const float mn = fmaxf(mx, ml[k].x), ref = mn == -INFINITY ? 0.0f : mn;
+            const float fa = __builtin_amdgcn_exp2f(mx - ref), fb = __builtin_amdgcn_exp2f(ml[k].x - ref);
+            sum = sum * fa + ml[k].y * fb;
+            o = o * fa + v[k] * fb;
+            mx = mn;
+        }
+    }
+    const int i = a.group.div(row), hq = h * (int)a.group.d + row - i * (int)a.group.d;
     store_out(a.out + (int64_t)(sq.r0 + i) * a.out_stride + (int64_t)hq * D + dt * 16 + 4 * (lane >> 4),
               o * (sum == 0.0f ? 0.0f : 1.0f / sum));
 }
 
 struct AttnPlan {
     int rt, row_tiles, splits;
-    int64_t blocks;
+    bool even;
+    int64_t blocks, join_blocks;
     size_t ws;
 };
+
+constexpr size_t kHeader = 4352;                   // before
+static_assert((kMaxShared + 1) * sizeof(int32_t) <= kHeader, "before fits its place");
+
+template <int D>
+static const void *attn_kernel(int rt, bool even) {
+    if (even)
+        return rt == 1 ? reinterpret_cast<const void *>(k_attn<D, 1, true>)
+                       : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, true>) : reinterpret_cast<const void *>(k_attn<D, 4, true>);
+    return rt == 1 ? reinterpret_cast<const void *>(k_attn<D, 1, false>)
+                   : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, false>) : reinterpret_cast<const void *>(k_attn<D, 4, false>);
+}
+static const void *attn_kernel(int dim, int rt, bool even) {
+    return dim == 64 ? attn_kernel<64>(rt, even)
+                     : dim == 128 ? attn_kernel<128>(rt, even) : dim == 192 ? attn_kernel<192>(rt, even) : attn_kernel<256>(rt, even);
+}
 
 static AttnPlan attn_plan(const nvfp4_kv8_cache *c, const nvfp4_kv8_seqs *s, int q_heads) {
     AttnPlan p{};
@@ -488,25 +684,44 @@ static AttnPlan attn_plan(const nvfp4_kv8_cache *c, const nvfp4_kv8_seqs *s, int
     const int64_t cap = (int64_t)s->max_pages * c->page_tokens;
     const int64_t len = s->max_kv_len > 0 && s->max_kv_len < cap ? s->max_kv_len : cap;
     const int64_t steps = (len + kStep - 1) / kStep;
-    int64_t want = ((int64_t)num_cus() * (p.rt == 1 ? 4 : 2) + units - 1) / units;
-    want = want < steps ? want : steps;
-    p.splits = (int)(want < 1 ? 1 : want);
-    p.blocks = units * p.splits;
-    p.ws = p.splits > 1 ? (size_t)(units * p.rt * p.splits) * (16 * c->head_dim + 32) * sizeof(float) : 0;
+    // even shares keep the step count in 32 bits
+    p.even = p.row_tiles == 1 && s->batch <= kMaxShared && units * ((cap + kStep - 1) / kStep + 1 + kSetup) < (1LL << 30);
+    const int64_t slots = (int64_t)num_cus() * blocks_per_cu(attn_kernel(c->head_dim, p.rt, p.even), 256, 0);
+    p.splits = 1;
+    bool pieces;
+    if (p.even) {
+        // one workgroup a slot of the device, or a step
+        p.blocks = slots < units * (steps + kSetup) ? slots : units * (steps + kSetup);
+        pieces = true;
+    } else {
+        int64_t want = units < slots ? (slots + units - 1) / units : 1;   // less than 2 * slots workgroups
+        want = want < steps ? want : steps;
+        p.splits = (int)(want < 1 ? 1 : want);
+        p.blocks = units * p.splits;
+        pieces = p.splits > 1;
+    }
+    p.join_blocks = pieces ? units * p.rt * (c->head_dim / 16) : 0;
+    p.ws = kHeader + (pieces ? (size_t)(p.blocks * 2 * p.rt) * (16 * c->head_dim + 32) * sizeof(float) : 0);
     return p;
 }
 
+template <int D, int RT, bool EVEN>
+static void launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((k_attn<D, RT, EVEN>), dim3((unsigned)p.blocks), dim3(256), 0, s, a);
+    if (p.join_blocks > 0)
+        hipLaunchKernelGGL((k_attn_join<D, RT, EVEN>), dim3((unsigned)p.join_blocks), dim3(64), 0, s, a, (int)p.blocks);
+}
 template <int D>
-static void launch_attn(const AttnPlan &p, const AttnArgs &a, int batch, hipStream_t s) {
-    if (p.rt == 1)
-        hipLaunchKernelGGL((k_attn<D, 1>), dim3((unsigned)p.blocks), dim3(256), 0, s, a);
-    else if (p.rt == 2)
-        hipLaunchKernelGGL((k_attn<D, 2>), dim3((unsigned)p.blocks), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_attn<D, 4>), dim3((unsigned)p.blocks), dim3(256), 0, s, a);
-    if (p.splits > 1)
-        hipLaunchKernelGGL(k_attn_join<D>, dim3((unsigned)(batch * a.c.heads * p.row_tiles * p.rt * (D / 16))), dim3(64), 0, s,
-                           a, p.row_tiles * p.rt);
+static void launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
+    if (p.even) {
+        if (p.rt == 1) launch_attn<D, 1, true>(p, a, s);
+        else if (p.rt == 2) launch_attn<D, 2, true>(p, a, s);
+        else launch_attn<D, 4, true>(p, a, s);
+    } else {
+        if (p.rt == 1) launch_attn<D, 1, false>(p, a, s);
+        else if (p.rt == 2) launch_attn<D, 2, false>(p, a, s);
+        else launch_attn<D, 4, false>(p, a, s);
+    }
 }
 
 }  // namespace nvfp4
@@ -523,8 +738,8 @@ static int attn_check(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, 
 
 extern "C" size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads) {
     if (attn_check(cache, seqs, q_heads, "kv8_attention_workspace_bytes")) return 0;
-    if (seqs->batch == 0 || seqs->rows == 0) return 256;
-    return 256 + attn_plan(cache, seqs, q_heads).ws;
+    if (seqs->batch == 0 || seqs->rows == 0) return kHeader;
+    return attn_plan(cache, seqs, q_heads).ws;
 }
 
 extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, float scale,
@@ -545,9 +760,9 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
         return fail(NVFP4_ERR_SHAPE, "%s: out_row_stride=%lld must be a multiple of 8 and >= q_heads * head_dim", who,
                     (long long)out_row_stride);
     const AttnPlan p = attn_plan(cache, seqs, q->heads);
-    if (p.blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
-    if (!workspace || ws_bytes < 256 + p.ws)
-        return fail(NVFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : 0, 256 + p.ws);
+    if (p.blocks > 2147483647LL || p.join_blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!workspace || ws_bytes < p.ws)
+        return fail(NVFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : 0, p.ws);
     if (!aligned(workspace, 256)) return fail(NVFP4_ERR_ALIGN, "%s: workspace not 256-byte aligned", who);
     AttnArgs a;
     a.q = view(q);
@@ -561,16 +776,17 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
     a.sinks = sinks;
     a.out = out;
     a.out_stride = out_row_stride;
-    a.group = q->heads / cache->kv_heads;
+    a.group = fast_div((uint32_t)(q->heads / cache->kv_heads));
     a.row_tiles = p.row_tiles;
     a.splits = p.splits;
-    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    a.before = static_cast<int32_t *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kHeader);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     switch (cache->head_dim) {
-        case 64: launch_attn<64>(p, a, seqs->batch, s); break;
-        case 128: launch_attn<128>(p, a, seqs->batch, s); break;
-        case 192: launch_attn<192>(p, a, seqs->batch, s); break;
-        default: launch_attn<256>(p, a, seqs->batch, s); break;
+        case 64: launch_attn<64>(p, a, s); break;
+        case 128: launch_attn<128>(p, a, s); break;
+        case 192: launch_attn<192>(p, a, s); break;
+        default: launch_attn<256>(p, a, s); break;
     }
     return check_launch(who);
 }
