@@ -9,8 +9,10 @@
 // Why fp64.  The drawn token is where a running sum over the vocabulary passes
 // u * total.  A relative error e of the sums moves every one of V borders, so a
 // draw changes with a probability up to about V * e: a few per cent in fp32 (V =
-// 150000), 1e-9 in fp64.  gfx950 runs fp64 FMAs at the fp32 rate, so the
-// exponentials (about 20 FMAs each) stay near the time the bytes take.
+// 150000), 1e-7 with the exponential below.  gfx950 runs fp64 FMAs at the fp32
+// rate, but its fp64 conversions, roundings and ldexp at a quarter of it: the
+// exponential is 14 full-rate fp64 operations, one conversion and two integer
+// operations.
 #include "common.hpp"
 
 namespace nvfp4 {
@@ -25,7 +27,8 @@ struct VerifyArgs {
     int32_t *accepted, *tokens, *next, *out_lens;
     int chunk, chunks;
     struct VPart *part;     // [batch][max_rows][1 or 2][chunks]
-    double *rest;           // [batch][chunks]: sums of max(p - q, 0)
+    double *rest;           // [batch][chunks]: sums of what is drawn from (draft logits given)
+    struct Decision *decided;   // [batch] (draft logits given)
 };
 
 struct VPart {
@@ -35,24 +38,32 @@ struct VPart {
     int idx;                // of the first maximum (-1: nothing above -inf)
 };
 
-// exp(x), x <= 0 (or NaN): relative error about 1e-14.
-__device__ __forceinline__ double exp_neg(double x) {
-    x = x < -800.0 ? -800.0 : x;
-    const double n = __builtin_rint(x * 1.44269504088896340736);
-    const double r = __builtin_fma(n, -0.69314718055994530942, x);   // |r| <= 0.347
-    double p = 1.0 / 39916800.0;                                     // Taylor to r^11
-    p = __builtin_fma(p, r, 1.0 / 3628800.0);
-    p = __builtin_fma(p, r, 1.0 / 362880.0);
-    p = __builtin_fma(p, r, 1.0 / 40320.0);
-    p = __builtin_fma(p, r, 1.0 / 5040.0);
-    p = __builtin_fma(p, r, 1.0 / 720.0);
-    p = __builtin_fma(p, r, 1.0 / 120.0);
-    p = __builtin_fma(p, r, 1.0 / 24.0);
-    p = __builtin_fma(p, r, 1.0 / 6.0);
-    p = __builtin_fma(p, r, 0.5);
+// 2^(d c) for d c in [-1022, 0]: d c = n + r with n an integer (the sum with 1.5 *
+// 2^52 holds it in its low bits), |r| <= 1/2, and 2^r = 1 + r P(r) with a
+// near-minimax P of degree 7, relative error 8.2e-13 (equal logits give equal terms,
+// the maximum exactly 1).  n is added to the exponent field.
+__device__ __forceinline__ double exp2_neg(double d, double c) {
+    const double t = __builtin_fma(d, c, 6755399441055744.0);
+    const double r = __builtin_fma(d, c, -(t - 6755399441055744.0));
+    double p = 1.3178936296684062e-06;
+    p = __builtin_fma(p, r, 1.5309156251773027e-05);
+    p = __builtin_fma(p, r, 0.0001540382545029347);
+    p = __builtin_fma(p, r, 0.001333345486025463);
+    p = __builtin_fma(p, r, 0.009618128616138841);
+    p = __builtin_fma(p, r, 0.05550410935266539);
+    p = __builtin_fma(p, r, 0.24022650698110554);
+    p = __builtin_fma(p, r, 0.6931471805482123);
     p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    return __builtin_ldexp(p, (int)n);
+    const uint64_t u = __builtin_bit_cast(uint64_t, p);
+    const uint32_t hi = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)u);
+}
+// exp((l - max) / T), c = log2(e) / T: 0 far below the maximum (and for l =
+// -inf), NaN for NaN.
+__device__ __forceinline__ double term(float l, float max, double c) {
+    const double d = (double)l - (double)max, y = d * c;
+    const double e = exp2_neg(y > -1020.0 ? d : 0.0, c);
+    return y > -1020.0 ? e : (y != y ? y : 0.0);
 }
 
 template <bool BF16>
@@ -72,10 +83,10 @@ __device__ __forceinline__ VSeq verify_seq(const VerifyArgs &a, int b) {
     q.n = min(q.full, a.max_rows);
     return q;
 }
-// 1 / T, or 0 for greedy.
+// log2(e) / T, or 0 for greedy.
 __device__ __forceinline__ double inv_temp(const VerifyArgs &a, int b) {
     const float t = a.temp ? a.temp[b] : 1.0f;
-    return t > 0.0f ? 1.0 / (double)t : 0.0;
+    return t > 0.0f && t < INFINITY ? 1.44269504088896340736 / (double)t : 0.0;
 }
 
 // A maximum with the lowest index among equals; NaN never wins.
@@ -96,13 +107,53 @@ __device__ __forceinline__ double shfl_up_f64(double v, int d) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// Elements e0 .. e0 + N - 1 of a row (-inf from `end` on); `vec`: rows are 16-byte
+// aligned and e0 * element size a multiple of the N elements' bytes or 16.
+template <bool BF16, int N>
+__device__ __forceinline__ void load_logits(const void *base, int64_t row, int e0, int end, bool vec, float (&x)[N]) {
+    if (vec && e0 + N <= end) {
+        if (BF16) {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + row + e0;
+            uint32_t w[N / 2];
+            if (N == 4) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                w[0] = v.x;
+                w[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < N / 8; ++i) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                    w[4 * i] = v.x;
+                    w[4 * i + 1] = v.y;
+                    w[4 * i + 2] = v.z;
+                    w[4 * i + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        } else {
+            const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + row + e0);
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 v = p[i];
+                x[4 * i] = v.x;
+                x[4 * i + 1] = v.y;
+                x[4 * i + 2] = v.z;
+                x[4 * i + 3] = v.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = e0 + i < end ? logit<BF16>(base, row + e0 + i) : -INFINITY;
+    }
+}
+
 // ------------------------------------------------------ partials of chunks --
 constexpr int kVThreads = 256;
 
-// PER elements a thread in groups of E (16 bytes); VEC: rows are 16-byte
-// aligned.
-template <bool BF16, int PER, bool VEC>
-__global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds) {
+// A chunk of kVThreads * PER elements; a thread's elements in groups of 16 bytes.
+template <bool BF16, int PER>
+__global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds, bool vec) {
     constexpr int E = BF16 ? 8 : 4;
     const int chunk = blockIdx.x % a.chunks;
     int w = blockIdx.x / a.chunks;
@@ -115,74 +166,75 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
     const int tid = threadIdx.x, c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
     const void *base = kind ? a.draft : a.logits;
     const int64_t row = (int64_t)(q.r0 + i) * (kind ? a.dstride : a.stride);
-    float x[PER];
+    float x[PER / E][E];
 #pragma unroll
-    for (int g = 0; g < PER / E; ++g) {
-        const int e0 = c0 + (g * kVThreads + tid) * E;
-        if (VEC && e0 + E <= c1) {
-            if (BF16) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + row + e0);
-                const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < E; ++j) x[g * E + j] = bf16_bits_to_f32(j & 1 ? p[j / 2] >> 16 : p[j / 2] & 0xFFFFu);
-            } else {
-                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + row + e0);
-                x[g * E] = v.x;
-                x[g * E + 1] = v.y;
-                x[g * E + 2] = v.z;
-                x[g * E + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < E; ++j) x[g * E + j] = e0 + j < c1 ? logit<BF16>(base, row + e0 + j) : -INFINITY;
-        }
-    }
+    for (int g = 0; g < PER / E; ++g) load_logits<BF16, E>(base, row, c0 + (g * kVThreads + tid) * E, c1, vec, x[g]);
+    const int id = kinds == 1 && i < q.n - 1 ? a.ids[q.r0 + i] : -1;
     float mx = -INFINITY;
-    int mi = -1;
+    bool nan = false;
 #pragma unroll
     for (int g = 0; g < PER / E; ++g)
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (x[g * E + j] > mx) {
-                mx = x[g * E + j];
-                mi = c0 + (g * kVThreads + tid) * E + j;
-            }
-    for (int m = 1; m < 64; m <<= 1) take_max(mx, mi, __shfl_xor(mx, m, 64), __shfl_xor(mi, m, 64));
+        for (int j = 0; j < E; ++j) {
+            mx = fmaxf(mx, x[g][j]);
+            nan |= x[g][j] != x[g][j];
+        }
     __shared__ float smax[kVThreads / 64];
-    __shared__ int sidx[kVThreads / 64];
+    __shared__ int sidx;
+    __shared__ bool snan[kVThreads / 64];
     __shared__ double ssum[kVThreads / 64];
+    nan = __any(nan);
+    const float own = mx;
+    for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m, 64));
     if ((tid & 63) == 0) {
         smax[tid >> 6] = mx;
-        sidx[tid >> 6] = mi;
+        snan[tid >> 6] = nan;
     }
+    if (tid == 0) sidx = 0x7FFFFFFF;
     __syncthreads();
-    mx = smax[0];
-    mi = sidx[0];
-    for (int v = 1; v < kVThreads / 64; ++v) take_max(mx, mi, smax[v], sidx[v]);
+#pragma unroll
+    for (int v = 0; v < kVThreads / 64; ++v) {
+        mx = fmaxf(mx, smax[v]);
+        nan |= snan[v];
+    }
+    // the first index that has the maximum
+    if (own == mx && mx > -INFINITY) {
+        int mi = 0x7FFFFFFF;
+#pragma unroll
+        for (int g = PER / E - 1; g >= 0; --g)
+#pragma unroll
+            for (int j = E - 1; j >= 0; --j) mi = x[g][j] == mx ? c0 + (g * kVThreads + tid) * E + j : mi;
+        atomicMin(&sidx, mi);
+    }
     double sum = 0.0;
     if (it > 0.0) {
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        if (kinds == 1 && i < q.n - 1) {
-            const int id = a.ids[q.r0 + i];
+        if (id >= c0 && id < c1) {
 #pragma unroll
             for (int g = 0; g < PER / E; ++g)
 #pragma unroll
                 for (int j = 0; j < E; ++j)
-                    if (c0 + (g * kVThreads + tid) * E + j == id) x[g * E + j] = -INFINITY;
+                    if (c0 + (g * kVThreads + tid) * E + j == id) x[g][j] = -INFINITY;
         }
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        // terms far below the maximum (and a NaN, which is noted) become 2^-1000,
+        // nothing beside its 1
+        const float low = (float)fmax((double)ref - 1000.0 / it, -3.0e38);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) sum += exp_neg(((double)x[j] - (double)ref) * it);
+        for (int g = 0; g < PER / E; ++g)
+#pragma unroll
+            for (int j = 0; j < E; ++j) sum += exp2_neg((double)fmaxf(x[g][j], low) - (double)ref, it);
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
         if ((tid & 63) == 0) ssum[tid >> 6] = sum;
-        __syncthreads();
-        sum = ssum[0];
-        for (int v = 1; v < kVThreads / 64; ++v) sum += ssum[v];
     }
+    __syncthreads();
     if (tid == 0) {
         VPart p;
-        p.sum = sum;
+        p.sum = 0.0;
+        if (it > 0.0 && mx > -INFINITY)
+            for (int v = 0; v < kVThreads / 64; ++v) p.sum += ssum[v];
+        if (nan) p.sum = NAN;
         p.max = mx;
-        p.idx = mi;
+        p.idx = mx > -INFINITY ? sidx : -1;
         a.part[((int64_t)(b * a.max_rows + i) * kinds + kind) * a.chunks + chunk] = p;
     }
 }
@@ -198,13 +250,13 @@ struct VRow {
 };
 __device__ __forceinline__ VRow join_chunks(const VPart *p, int chunks, double it, int lane) {
     VRow r{0.0, -INFINITY, -1};
-    for (int c = lane; c < chunks; c += 64) take_max(r.max, r.idx, p[c].max, p[c].idx);
+    const VPart mine = p[min(lane, chunks - 1)];       // of the first 64 chunks
+    if (lane < chunks) take_max(r.max, r.idx, mine.max, mine.idx);
+    for (int c = lane + 64; c < chunks; c += 64) take_max(r.max, r.idx, p[c].max, p[c].idx);
     for (int m = 1; m < 64; m <<= 1) take_max(r.max, r.idx, __shfl_xor(r.max, m, 64), __shfl_xor(r.idx, m, 64));
     if (it > 0.0 && r.max > -INFINITY && r.max < INFINITY) {
-        for (int c = lane; c < chunks; c += 64) {
-            const double s = p[c].sum;
-            if (p[c].max > -INFINITY || !(s == 0.0)) r.sum += s * exp_neg(((double)p[c].max - (double)r.max) * it);
-        }
+        if (lane < chunks) r.sum = mine.sum * term(mine.max, r.max, it);
+        for (int c = lane + 64; c < chunks; c += 64) r.sum += p[c].sum * term(p[c].max, r.max, it);
         for (int m = 1; m < 64; m <<= 1) r.sum += shfl_xor_f64(r.sum, m);
     }
     return r;
@@ -230,17 +282,20 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int i = wave; i < q.n; i += kDecideThreads / 64) {
         const VPart *p = a.part + ((int64_t)(b * a.max_rows + i) * kinds) * a.chunks;
+        const bool last = i == q.n - 1;
+        const int64_t row = q.r0 + i;
+        const int id = last ? -1 : a.ids[row];
+        const bool in = id >= 0 && id < a.vocab;
+        const float ld = in ? logit<BF16>(a.logits, row * a.stride + id) : 0.0f;
+        const float lq = in && kinds == 2 ? logit<BF16>(a.draft, row * a.dstride + id) : 0.0f;
+        const float ua = last ? 0.0f : a.ua[row];
         VRow rp = join_chunks(p, a.chunks, it, lane);
         VRow rq{0.0, -INFINITY, -1};
-        const bool last = i == q.n - 1;
         int stop = 1;
         if (!last) {
-            const int64_t row = q.r0 + i;
-            const int id = a.ids[row];
-            const bool in = id >= 0 && id < a.vocab;
             double wd = 0.0;                          // the draft's term of the sum
             if (in && it > 0.0 && rp.max > -INFINITY && rp.max < INFINITY) {
-                wd = exp_neg(((double)logit<BF16>(a.logits, row * a.stride + id) - (double)rp.max) * it);
+                wd = term(ld, rp.max, it);
                 if (kinds == 1) rp.sum += wd;
             }
             if (kinds == 2) rq = join_chunks(p + a.chunks, a.chunks, it, lane);
@@ -250,8 +305,8 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
                 const double pd = wd / rp.sum;
                 double qd = 1.0;
                 if (kinds == 2 && rq.finite())
-                    qd = exp_neg(((double)logit<BF16>(a.draft, row * a.dstride + id) - (double)rq.max) * it) / rq.sum;
-                stop = !((double)a.ua[row] * qd < pd);
+                    qd = term(lq, rq.max, it) / rq.sum;
+                stop = !((double)ua * qd < pd);
             }
         }
         if (lane == 0) {
@@ -283,33 +338,45 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
     __syncthreads();
 }
 
-// Weight of token e under the decision.
-template <bool BF16>
-__device__ __forceinline__ double weight(const VerifyArgs &a, const Decision &d, int mode, int64_t prow, int64_t qrow, int e,
-                                         double it) {
-    if (mode == kWithout && e == d.draft) return 0.0;
-    const double p = exp_neg(((double)logit<BF16>(a.logits, prow + e) - (double)d.pmax) * it);
-    if (mode != kRest) return p;
-    const double r = p / d.psum - exp_neg(((double)logit<BF16>(a.draft, qrow + e) - (double)d.qmax) * it) / d.qsum;
-    return r > 0.0 ? r : 0.0;
+// Weights of a thread's N elements e0 .. under the decision (0 from `end` on).
+template <bool BF16, int N>
+__device__ __forceinline__ void weights(const VerifyArgs &a, const Decision &d, int mode, int64_t row, int e0, int end,
+                                        double it, bool vec, double (&w)[N]) {
+    float x[N];
+    load_logits<BF16, N>(a.logits, row * a.stride, e0, end, vec, x);
+    if (mode == kRest) {
+        float y[N];
+        load_logits<BF16, N>(a.draft, row * a.dstride, e0, end, vec, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double r = term(x[i], d.pmax, it) / d.psum - term(y[i], d.qmax, it) / d.qsum;
+            w[i] = e0 + i < end && r > 0.0 ? r : 0.0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = mode == kWithout && e0 + i == d.draft ? 0.0 : term(x[i], d.pmax, it);
+    }
 }
 
-// Sums per chunk of what is drawn from after a fallen draft (draft logits
-// given): max(p - q, 0), or p without the draft where q has no finite sum.
-template <bool BF16>
-__global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a) {
+// With draft logits: the decisions, and per chunk the sums of what is drawn from
+// after a fallen draft, max(p - q, 0), or p without the draft where q has no finite
+// sum.
+template <bool BF16, int PER>
+__global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a, bool vec) {
+    constexpr int N = PER * kVThreads / kDecideThreads;
     const int chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks;
     const VSeq q = verify_seq(a, b);
     if (q.n == 0) return;
     const double it = inv_temp(a, b);
     Decision d;
     decide<BF16>(a, b, q, it, 2, d);
+    if (chunk == 0 && threadIdx.x == 0) a.decided[b] = d;
     if (d.mode != kRest && d.mode != kWithout) return;
-    const int64_t row = q.r0 + d.row;
     const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
-    double sum = 0.0;
-    for (int e = c0 + (int)threadIdx.x; e < c1; e += kDecideThreads)
-        sum += weight<BF16>(a, d, d.mode, row * a.stride, row * a.dstride, e, it);
+    double w[N], sum = 0.0;
+    weights<BF16, N>(a, d, d.mode, q.r0 + d.row, c0 + (int)threadIdx.x * N, c1, it, vec, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += w[i];
     for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
     __shared__ double ssum[kDecideThreads / 64];
     if ((threadIdx.x & 63) == 0) ssum[threadIdx.x >> 6] = sum;
@@ -320,9 +387,16 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a) {
     }
 }
 
+__device__ __forceinline__ double lane_f64(double v, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __shfl((int)(uint32_t)u, l, 64), hi = __shfl((int)(uint32_t)(u >> 32), l, 64);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // One workgroup per sequence: the decision, the draw, the outputs.
-template <bool BF16>
-__global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, int kinds) {
+template <bool BF16, int PER>
+__global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, int kinds, bool vec) {
+    constexpr int N = PER * kVThreads / kDecideThreads;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const VSeq q = verify_seq(a, b);
     if (q.n == 0) {
@@ -335,36 +409,38 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
     }
     const double it = inv_temp(a, b);
     Decision d;
-    decide<BF16>(a, b, q, it, kinds, d);
-    __shared__ int schunk, stoken;
-    __shared__ double starget;
+    if (kinds == 2)
+        d = a.decided[b];
+    else
+        decide<BF16>(a, b, q, it, 1, d);
+    __shared__ int schunk, smode, first_hit, last_live;
+    __shared__ double starget, wsum[kDecideThreads / 64];
     int token = d.best;
     if (d.mode != kGreedy) {
         const VPart *part = a.part + ((int64_t)(b * a.max_rows + d.row) * kinds) * a.chunks;
         const double *rest = a.rest + (int64_t)b * a.chunks;
-        const int64_t prow = (int64_t)(q.r0 + d.row) * a.stride, qrow = (int64_t)(q.r0 + d.row) * a.dstride;
-        int mode = d.mode;
         if (wave == 0) {
             // chunk weights, their running sum, and the chunk that passes u * total
             // (outright drafts: the partial sums are already without the draft)
-            auto chunk_weight = [&](int c, int m) {
+            int mode = d.mode;
+            auto chunk_weight = [&](int c) {
                 if (c >= a.chunks) return 0.0;
-                if (m == kRest || (m == kWithout && kinds == 2)) return rest[c];
-                return part[c].max > -INFINITY ? part[c].sum * exp_neg(((double)part[c].max - (double)d.pmax) * it) : 0.0;
+                if (mode == kRest || (mode == kWithout && kinds == 2)) return rest[c];
+                return part[c].max > -INFINITY ? part[c].sum * term(part[c].max, d.pmax, it) : 0.0;
             };
-            double total = 0.0;
-            for (int c = lane; c < a.chunks; c += 64) total += chunk_weight(c, mode);
+            double mine = chunk_weight(lane), total = mine;
+            for (int c = lane + 64; c < a.chunks; c += 64) total += chunk_weight(c);
             for (int m = 1; m < 64; m <<= 1) total += shfl_xor_f64(total, m);
             if (mode == kRest && !(total > 0.0)) {    // p and q are equal: draw from p
                 mode = kFromP;
                 total = d.psum;
+                mine = chunk_weight(lane);
             }
             const double target = (double)a.us[b] * total;
-            double before = 0.0, best_before = 0.0;
+            double before = 0.0, from = 0.0, live_from = 0.0;
             int hit = -1, live = -1;                  // the chunk found; the last one with weight
-            double live_before = 0.0;
             for (int c0 = 0; c0 < a.chunks && hit < 0; c0 += 64) {
-                const double own = chunk_weight(c0 + lane, mode);
+                const double own = c0 == 0 ? mine : chunk_weight(c0 + lane);
                 double run = own;
                 for (int s = 1; s < 64; s <<= 1) {
                     const double o = shfl_up_f64(run, s);
@@ -372,76 +448,60 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
                 }
                 const uint64_t pass = __ballot(before + run > target && own > 0.0), some = __ballot(own > 0.0);
                 const double excl = before + run - own;
-                auto lane_value = [&](double v, int l) {
-                    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-                    const uint32_t lo = __shfl((int)(uint32_t)u, l, 64), hi = __shfl((int)(uint32_t)(u >> 32), l, 64);
-                    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-                };
                 if (pass) {
-                    const int l = __builtin_ctzll(pass);
-                    hit = c0 + l;
-                    best_before = lane_value(excl, l);
+                    hit = c0 + __builtin_ctzll(pass);
+                    from = lane_f64(excl, hit - c0);
                 }
                 if (some) {
-                    const int l = 63 - __builtin_clzll(some);
-                    live = c0 + l;
-                    live_before = lane_value(excl, l);
+                    live = c0 + 63 - __builtin_clzll(some);
+                    live_from = lane_f64(excl, live - c0);
                 }
-                before = lane_value(before + run, 63);
+                before = lane_f64(before + run, 63);
             }
             if (hit < 0) {                            // rounding at the very end
                 hit = live;
-                best_before = live_before;
+                from = live_from;
             }
             if (lane == 0) {
                 schunk = hit;
-                starget = target - best_before;
-                stoken = mode;
+                starget = target - from;
+                smode = mode;
+                first_hit = 0x7FFFFFFF;
+                last_live = -1;
             }
         }
         __syncthreads();
-        mode = stoken;
         const int chunk = schunk;
-        const double target = starget;
-        __syncthreads();
         if (chunk >= 0) {
-            // scan of the chunk: contiguous elements per thread
-            const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
-            const int per = (a.chunk + kDecideThreads - 1) / kDecideThreads;
-            const int e0 = c0 + tid * per, e1 = min(e0 + per, c1);
-            double own = 0.0;
+            // the chunk again: N elements a thread, their running sum
+            const double target = starget;
+            const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab), e0 = c0 + tid * N;
+            double w[N], own = 0.0;
+            weights<BF16, N>(a, d, smode, q.r0 + d.row, e0, c1, it, vec, w);
             int last = -1;
-            for (int e = e0; e < e1; ++e) {
-                const double v = weight<BF16>(a, d, mode, prow, qrow, e, it);
-                own += v;
-                if (v > 0.0) last = e;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                own += w[i];
+                last = w[i] > 0.0 ? e0 + i : last;
             }
             double run = own;
             for (int s = 1; s < 64; s <<= 1) {
                 const double o = shfl_up_f64(run, s);
                 if (lane >= s) run += o;
             }
-            __shared__ double wsum[kDecideThreads / 64];
-            __shared__ int first_hit, last_live;
             if (lane == 63) wsum[wave] = run;
-            if (tid == 0) {
-                first_hit = 0x7FFFFFFF;
-                last_live = -1;
-            }
             __syncthreads();
-            double before = run - own;
-            for (int i = 0; i < wave; ++i) before += wsum[i];
+            double sum = run - own;
+            for (int i = 0; i < wave; ++i) sum += wsum[i];
             if (last >= 0) atomicMax(&last_live, last);
-            if (before + own > target && own > 0.0) {
-                double s = before;
-                for (int e = e0; e < e1; ++e) {
-                    const double v = weight<BF16>(a, d, mode, prow, qrow, e, it);
-                    s += v;
-                    if (v > 0.0 && s > target) {
-                        atomicMin(&first_hit, e);
-                        break;
-                    }
+            if (sum + own > target && own > 0.0) {
+                int at = 0x7FFFFFFF;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    sum += w[i];
+                    at = min(at, w[i] > 0.0 && sum > target ? e0 + i : 0x7FFFFFFF);
                 }
+                if (at != 0x7FFFFFFF) atomicMin(&first_hit, at);
             }
             __syncthreads();
             token = first_hit != 0x7FFFFFFF ? first_hit : (last_live >= 0 ? last_live : d.best);
@@ -471,30 +531,27 @@ static VerifyPlan verify_plan(int batch, int max_rows, int vocab, bool draft) {
     p.chunk = kVThreads * p.per;
     p.chunks = (vocab + p.chunk - 1) / p.chunk;
     p.part = (size_t)rows * (draft ? 2 : 1) * p.chunks * sizeof(VPart);
-    p.ws = p.part + (draft ? (size_t)batch * p.chunks * sizeof(double) : 0);
+    p.ws = p.part + (draft ? (size_t)batch * (p.chunks * sizeof(double) + sizeof(Decision)) : 0);
     return p;
 }
 
 template <bool BF16, int PER>
-static void launch_stats(const VerifyArgs &a, int kinds, bool vec, hipStream_t s) {
+static void launch_verify(const VerifyArgs &a, bool draft, bool vec, hipStream_t s) {
+    const int kinds = draft ? 2 : 1;
     const unsigned grid = (unsigned)((int64_t)a.batch * a.max_rows * kinds * a.chunks);
-    if (vec)
-        hipLaunchKernelGGL((k_verify_stats<BF16, PER, true>), dim3(grid), dim3(kVThreads), 0, s, a, kinds);
-    else
-        hipLaunchKernelGGL((k_verify_stats<BF16, PER, false>), dim3(grid), dim3(kVThreads), 0, s, a, kinds);
+    hipLaunchKernelGGL((k_verify_stats<BF16, PER>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
+    if (draft)
+        hipLaunchKernelGGL((k_verify_rest<BF16, PER>), dim3((unsigned)(a.batch * a.chunks)), dim3(kDecideThreads), 0, s, a, vec);
+    hipLaunchKernelGGL((k_verify_pick<BF16, PER>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
 }
 
 template <bool BF16>
 static void launch_verify(const VerifyArgs &a, int per, bool draft, bool vec, hipStream_t s) {
-    const int kinds = draft ? 2 : 1;
     switch (per) {
-        case 8: launch_stats<BF16, 8>(a, kinds, vec, s); break;
-        case 16: launch_stats<BF16, 16>(a, kinds, vec, s); break;
-        default: launch_stats<BF16, 32>(a, kinds, vec, s); break;
+        case 8: launch_verify<BF16, 8>(a, draft, vec, s); break;
+        case 16: launch_verify<BF16, 16>(a, draft, vec, s); break;
+        default: launch_verify<BF16, 32>(a, draft, vec, s); break;
     }
-    if (draft)
-        hipLaunchKernelGGL((k_verify_rest<BF16>), dim3((unsigned)(a.batch * a.chunks)), dim3(kDecideThreads), 0, s, a);
-    hipLaunchKernelGGL((k_verify_pick<BF16>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds);
 }
 
 }  // namespace nvfp4
@@ -568,6 +625,7 @@ extern "C" int verify_drafts(const void *logits, int32_t logits_dtype, int64_t r
     a.chunks = p.chunks;
     a.part = static_cast<VPart *>(workspace);
     a.rest = reinterpret_cast<double *>(static_cast<char *>(workspace) + p.part);
+    a.decided = reinterpret_cast<Decision *>(a.rest + (size_t)batch * p.chunks);
     const bool vec = aligned(logits, 16) && row_stride * el % 16 == 0 &&
                      (!draft_logits || (aligned(draft_logits, 16) && draft_stride * el % 16 == 0));
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
