@@ -27,13 +27,15 @@ struct VerifyArgs {
     int32_t *accepted, *tokens, *next, *out_lens;
     int chunk, chunks;
     struct VPart *part;     // [batch][max_rows][1 or 2][chunks]
-    double *rest;           // [batch][chunks]: sums of what is drawn from (draft logits given)
-    struct Decision *decided;   // [batch] (draft logits given)
+    bool exact;             // the partials' sums are fp64
+    bool second;            // k_verify_rest runs: decisions and the drawn row's sums
+    double *rest;           // [batch][chunks]: sums of what is drawn from (second)
+    struct Decision *decided;   // [batch] (second)
 };
 
 struct VPart {
-    double sum;             // of exp((l - max) / T) over the chunk; without the draft's own
-                            // term where the draft is outright
+    double sum;             // of exp((l - max) / T) over the chunk (fp64 sums of outright
+                            // drafts: without the draft's own term)
     float max;
     int idx;                // of the first maximum (-1: nothing above -inf)
 };
@@ -152,7 +154,10 @@ __device__ __forceinline__ void load_logits(const void *base, int64_t row, int e
 constexpr int kVThreads = 256;
 
 // A chunk of kVThreads * PER elements; a thread's elements in groups of 16 bytes.
-template <bool BF16, int PER>
+// EXACT: fp64 terms.  Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5
+// (30 binary digits of an argument, 32 fp32 additions), which decides every draft
+// but those next to the border (see decide), and the drawn row is summed again.
+template <bool BF16, int PER, bool EXACT>
 __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds, bool vec) {
     constexpr int E = BF16 ? 8 : 4;
     const int chunk = blockIdx.x % a.chunks;
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
     float x[PER / E][E];
 #pragma unroll
     for (int g = 0; g < PER / E; ++g) load_logits<BF16, E>(base, row, c0 + (g * kVThreads + tid) * E, c1, vec, x[g]);
-    const int id = kinds == 1 && i < q.n - 1 ? a.ids[q.r0 + i] : -1;
+    const int id = EXACT && kinds == 1 && i < q.n - 1 ? a.ids[q.r0 + i] : -1;
     float mx = -INFINITY;
     bool nan = false;
 #pragma unroll
@@ -216,6 +221,15 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
                     if (c0 + (g * kVThreads + tid) * E + j == id) x[g][j] = -INFINITY;
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
+        if (!EXACT) {
+            const float c = (float)it;
+            float part = 0.0f;
+#pragma unroll
+            for (int g = 0; g < PER / E; ++g)
+#pragma unroll
+                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f((x[g][j] - ref) * c);
+            sum = part;
+        } else {
         // terms far below the maximum (and a NaN, which is noted) become 2^-1000,
         // nothing beside its 1
         const float low = (float)fmax((double)ref - 1000.0 / it, -3.0e38);
@@ -223,6 +237,7 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
         for (int g = 0; g < PER / E; ++g)
 #pragma unroll
             for (int j = 0; j < E; ++j) sum += exp2_neg((double)fmaxf(x[g][j], low) - (double)ref, it);
+        }
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
         if ((tid & 63) == 0) ssum[tid >> 6] = sum;
     }
@@ -273,12 +288,36 @@ struct Decision {
 constexpr int kMaxRows = 64;
 constexpr int kDecideThreads = 512;
 
-// One workgroup of kDecideThreads: where sequence b stops and how its token is
-// drawn.
+// The sum of a whole row in fp64, by the whole workgroup.
 template <bool BF16>
-__device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q, double it, int kinds, Decision &d) {
+__device__ __forceinline__ double row_sum(const VerifyArgs &a, int64_t row, float max, double it, bool vec) {
+    __shared__ double part[kDecideThreads / 64];
+    double sum = 0.0;
+    for (int e0 = threadIdx.x * 8; e0 < a.vocab; e0 += kDecideThreads * 8) {
+        float x[8];
+        load_logits<BF16, 8>(a.logits, row * a.stride, e0, a.vocab, vec, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += term(x[i], max, it);
+    }
+    for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int i = 0; i < kDecideThreads / 64; ++i) sum += part[i];
+    return sum;
+}
+
+// One workgroup of kDecideThreads: where sequence b stops and how its token is
+// drawn.  The test u q(d) < p(d) is u wq sum_p < wd sum_q with the drafts' terms wd,
+// wq; with fp32 sums a test whose sides agree to 2^-16 is made again with the row's
+// fp64 sum.
+template <bool BF16>
+__device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q, double it, int kinds, bool vec, Decision &d) {
     __shared__ VRow sp[kMaxRows], sq[kMaxRows];
-    __shared__ int sstop[kMaxRows];
+    __shared__ double swd[kMaxRows];
+    __shared__ float sua[kMaxRows];
+    __shared__ int sstop[kMaxRows], sid[kMaxRows];    // 2: too close to tell
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int i = wave; i < q.n; i += kDecideThreads / 64) {
         const VPart *p = a.part + ((int64_t)(b * a.max_rows + i) * kinds) * a.chunks;
@@ -291,37 +330,46 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
         const float ua = last ? 0.0f : a.ua[row];
         VRow rp = join_chunks(p, a.chunks, it, lane);
         VRow rq{0.0, -INFINITY, -1};
+        double wd = 0.0;                              // the draft's term of the sum
         int stop = 1;
         if (!last) {
-            double wd = 0.0;                          // the draft's term of the sum
             if (in && it > 0.0 && rp.max > -INFINITY && rp.max < INFINITY) {
                 wd = term(ld, rp.max, it);
-                if (kinds == 1) rp.sum += wd;
+                if (kinds == 1 && a.exact) rp.sum += wd;
             }
             if (kinds == 2) rq = join_chunks(p + a.chunks, a.chunks, it, lane);
             if (!(it > 0.0) || !rp.finite()) {
                 stop = id != max(rp.idx, 0);
             } else if (in) {
-                const double pd = wd / rp.sum;
-                double qd = 1.0;
-                if (kinds == 2 && rq.finite())
-                    qd = term(lq, rq.max, it) / rq.sum;
-                stop = !((double)ua * qd < pd);
+                double lhs = (double)ua * rp.sum, rhs = wd;
+                if (kinds == 2 && rq.finite()) {
+                    lhs *= term(lq, rq.max, it);
+                    rhs *= rq.sum;
+                }
+                stop = !(lhs < rhs);
+                if (!a.exact && fabs(lhs - rhs) <= rhs * 0x1p-16) stop = 2;
             }
         }
         if (lane == 0) {
             sp[i] = rp;
             sq[i] = rq;
+            swd[i] = wd;
+            sua[i] = ua;
+            sid[i] = id;
             sstop[i] = stop;
         }
     }
     __syncthreads();
     int at = 0;
-    while (!sstop[at]) ++at;                          // the last row always stops
+    for (;; ++at) {                                   // the last row always stops
+        int stop = sstop[at];
+        if (stop == 2) stop = !((double)sua[at] * row_sum<BF16>(a, q.r0 + at, sp[at].max, it, vec) < swd[at]);
+        if (stop) break;
+    }
     const bool last = at == q.n - 1;
     const VRow rp = sp[at], rq = sq[at];
     d.row = at;
-    d.draft = last ? -1 : a.ids[q.r0 + at];
+    d.draft = sid[at];
     d.best = max(rp.idx, 0);
     d.pmax = rp.max;
     d.psum = rp.sum;
@@ -347,9 +395,10 @@ __device__ __forceinline__ void weights(const VerifyArgs &a, const Decision &d, 
     if (mode == kRest) {
         float y[N];
         load_logits<BF16, N>(a.draft, row * a.dstride, e0, end, vec, y);
+        const double ip = 1.0 / d.psum, iq = 1.0 / d.qsum;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const double r = term(x[i], d.pmax, it) / d.psum - term(y[i], d.qmax, it) / d.qsum;
+            const double r = term(x[i], d.pmax, it) * ip - term(y[i], d.qmax, it) * iq;
             w[i] = e0 + i < end && r > 0.0 ? r : 0.0;
         }
     } else {
@@ -358,20 +407,19 @@ __device__ __forceinline__ void weights(const VerifyArgs &a, const Decision &d, 
     }
 }
 
-// With draft logits: the decisions, and per chunk the sums of what is drawn from
-// after a fallen draft, max(p - q, 0), or p without the draft where q has no finite
-// sum.
+// The decisions, and per chunk the fp64 sums of what is drawn from: max(p - q, 0),
+// or p, or p without the draft.
 template <bool BF16, int PER>
-__global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a, bool vec) {
+__global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a, int kinds, bool vec) {
     constexpr int N = PER * kVThreads / kDecideThreads;
     const int chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks;
     const VSeq q = verify_seq(a, b);
     if (q.n == 0) return;
     const double it = inv_temp(a, b);
     Decision d;
-    decide<BF16>(a, b, q, it, 2, d);
+    decide<BF16>(a, b, q, it, kinds, vec, d);
     if (chunk == 0 && threadIdx.x == 0) a.decided[b] = d;
-    if (d.mode != kRest && d.mode != kWithout) return;
+    if (d.mode == kGreedy) return;
     const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
     double w[N], sum = 0.0;
     weights<BF16, N>(a, d, d.mode, q.r0 + d.row, c0 + (int)threadIdx.x * N, c1, it, vec, w);
@@ -409,10 +457,10 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
     }
     const double it = inv_temp(a, b);
     Decision d;
-    if (kinds == 2)
+    if (a.second)
         d = a.decided[b];
     else
-        decide<BF16>(a, b, q, it, 1, d);
+        decide<BF16>(a, b, q, it, kinds, vec, d);
     __shared__ int schunk, smode, first_hit, last_live;
     __shared__ double starget, wsum[kDecideThreads / 64];
     int token = d.best;
@@ -421,11 +469,12 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
         const double *rest = a.rest + (int64_t)b * a.chunks;
         if (wave == 0) {
             // chunk weights, their running sum, and the chunk that passes u * total
-            // (outright drafts: the partial sums are already without the draft)
+            // (the partials of outright drafts are already without the draft)
             int mode = d.mode;
+            bool again = a.second;
             auto chunk_weight = [&](int c) {
                 if (c >= a.chunks) return 0.0;
-                if (mode == kRest || (mode == kWithout && kinds == 2)) return rest[c];
+                if (again) return rest[c];
                 return part[c].max > -INFINITY ? part[c].sum * term(part[c].max, d.pmax, it) : 0.0;
             };
             double mine = chunk_weight(lane), total = mine;
@@ -433,6 +482,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
             for (int m = 1; m < 64; m <<= 1) total += shfl_xor_f64(total, m);
             if (mode == kRest && !(total > 0.0)) {    // p and q are equal: draw from p
                 mode = kFromP;
+                again = false;
                 total = d.psum;
                 mine = chunk_weight(lane);
             }
@@ -518,6 +568,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
 
 struct VerifyPlan {
     int per, chunk, chunks;
+    bool exact, second;
     size_t part, ws;
 };
 
@@ -531,7 +582,13 @@ static VerifyPlan verify_plan(int batch, int max_rows, int vocab, bool draft) {
     p.chunk = kVThreads * p.per;
     p.chunks = (vocab + p.chunk - 1) / p.chunk;
     p.part = (size_t)rows * (draft ? 2 : 1) * p.chunks * sizeof(VPart);
-    p.ws = p.part + (draft ? (size_t)batch * (p.chunks * sizeof(double) + sizeof(Decision)) : 0);
+    // Outright drafts: fp32 partials and a second pass over the drawn rows once
+    // the chunks fill the device several times over (337 rows of 151936: 69 us with
+    // fp64 partials of every row), fp64 partials and no second pass below (4 rows:
+    // 15.7 us).
+    p.exact = draft || p.per < 32;
+    p.second = draft || !p.exact;
+    p.ws = p.part + (p.second ? (size_t)batch * (p.chunks * sizeof(double) + sizeof(Decision)) : 0);
     return p;
 }
 
@@ -539,9 +596,13 @@ template <bool BF16, int PER>
 static void launch_verify(const VerifyArgs &a, bool draft, bool vec, hipStream_t s) {
     const int kinds = draft ? 2 : 1;
     const unsigned grid = (unsigned)((int64_t)a.batch * a.max_rows * kinds * a.chunks);
-    hipLaunchKernelGGL((k_verify_stats<BF16, PER>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
-    if (draft)
-        hipLaunchKernelGGL((k_verify_rest<BF16, PER>), dim3((unsigned)(a.batch * a.chunks)), dim3(kDecideThreads), 0, s, a, vec);
+    if (a.exact)
+        hipLaunchKernelGGL((k_verify_stats<BF16, PER, true>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
+    else if constexpr (PER == 32)
+        hipLaunchKernelGGL((k_verify_stats<BF16, PER, false>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
+    if (a.second)
+        hipLaunchKernelGGL((k_verify_rest<BF16, PER>), dim3((unsigned)(a.batch * a.chunks)), dim3(kDecideThreads), 0, s, a, kinds,
+                           vec);
     hipLaunchKernelGGL((k_verify_pick<BF16, PER>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
 }
 
@@ -623,6 +684,8 @@ extern "C" int verify_drafts(const void *logits, int32_t logits_dtype, int64_t r
     a.out_lens = out_kv_lens;
     a.chunk = p.chunk;
     a.chunks = p.chunks;
+    a.exact = p.exact;
+    a.second = p.second;
     a.part = static_cast<VPart *>(workspace);
     a.rest = reinterpret_cast<double *>(static_cast<char *>(workspace) + p.part);
     a.decided = reinterpret_cast<Decision *>(a.rest + (size_t)batch * p.chunks);
