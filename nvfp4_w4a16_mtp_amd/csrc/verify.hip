@@ -25,13 +25,15 @@ struct VerifyArgs {
     const float *temp, *ua, *us;
     const int32_t *lens;
     int32_t *accepted, *tokens, *next, *out_lens;
-    int chunk, chunks;
+    int chunks;             // of a row, kChunk elements each
     struct VPart *part;     // [batch][max_rows][1 or 2][chunks]
     bool exact;             // the partials' sums are fp64
-    bool second;            // k_verify_rest runs: decisions and the drawn row's sums
+    bool second;            // k_verify_decide and k_verify_rest run
     double *rest;           // [batch][chunks]: sums of what is drawn from (second)
     struct Decision *decided;   // [batch] (second)
 };
+
+constexpr int kChunk = 2048;
 
 struct VPart {
     double sum;             // of exp((l - max) / T) over the chunk (fp64 sums of outright
@@ -153,103 +155,115 @@ __device__ __forceinline__ void load_logits(const void *base, int64_t row, int e
 // ------------------------------------------------------ partials of chunks --
 constexpr int kVThreads = 256;
 
-// A chunk of kVThreads * PER elements; a thread's elements in groups of 16 bytes.
-// EXACT: fp64 terms.  Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5
-// (30 binary digits of an argument, 32 fp32 additions), which decides every draft
-// but those next to the border (see decide), and the drawn row is summed again.
-template <bool BF16, int PER, bool EXACT>
+// A chunk is taken by WAVES wavefronts, kChunk / (64 * WAVES) elements a lane in
+// groups of 16 bytes.  WAVES = 1: no barriers, the loads of a workgroup's four
+// chunks overlap with each other's sums (many rows).  WAVES = 4: a quarter of the
+// terms per lane (few rows, where one chunk's time counts).  EXACT: fp64 terms.
+// Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5 (30 binary digits
+// of an argument, 32 fp32 additions), which decides every draft but those next to
+// the border (see decide), and the drawn row is summed again.
+template <bool BF16, int WAVES, bool EXACT>
 __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds, bool vec) {
-    constexpr int E = BF16 ? 8 : 4;
-    const int chunk = blockIdx.x % a.chunks;
-    int w = blockIdx.x / a.chunks;
-    const int kind = w % kinds;                       // 0 target, 1 draft
-    w /= kinds;
-    const int i = w % a.max_rows, b = w / a.max_rows;
+    constexpr int E = BF16 ? 8 : 4, PER = kChunk / (64 * WAVES), G = PER / E, T = 64 * WAVES;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int blocks = WAVES == 1 ? (a.chunks + 3) / 4 : a.chunks;
+    int w = blockIdx.x / blocks;
+    const int chunk = WAVES == 1 ? (blockIdx.x - w * blocks) * 4 + wave : blockIdx.x - w * blocks;
+    const int kind = kinds == 2 ? w & 1 : 0;          // 0 target, 1 draft
+    if (kinds == 2) w >>= 1;
+    const int b = w / a.max_rows, i = w - b * a.max_rows;
     const VSeq q = verify_seq(a, b);
-    if (i >= q.n || (kind == 1 && i == q.n - 1)) return;
-    const double it = inv_temp(a, b);
-    const int tid = threadIdx.x, c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
+    if (i >= q.n || (kind == 1 && i == q.n - 1) || chunk >= a.chunks) return;
+    const int tid = WAVES == 1 ? lane : (int)threadIdx.x, c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab);
     const void *base = kind ? a.draft : a.logits;
     const int64_t row = (int64_t)(q.r0 + i) * (kind ? a.dstride : a.stride);
-    float x[PER / E][E];
+    float x[G][E];
 #pragma unroll
-    for (int g = 0; g < PER / E; ++g) load_logits<BF16, E>(base, row, c0 + (g * kVThreads + tid) * E, c1, vec, x[g]);
+    for (int g = 0; g < G; ++g) load_logits<BF16, E>(base, row, c0 + (g * T + tid) * E, c1, vec, x[g]);
+    const double it = inv_temp(a, b);
     const int id = EXACT && kinds == 1 && i < q.n - 1 ? a.ids[q.r0 + i] : -1;
     float mx = -INFINITY;
     bool nan = false;
 #pragma unroll
-    for (int g = 0; g < PER / E; ++g)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             mx = fmaxf(mx, x[g][j]);
             nan |= x[g][j] != x[g][j];
         }
-    __shared__ float smax[kVThreads / 64];
-    __shared__ int sidx;
-    __shared__ bool snan[kVThreads / 64];
-    __shared__ double ssum[kVThreads / 64];
-    nan = __any(nan);
     const float own = mx;
+    nan = __any(nan);
     for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m, 64));
-    if ((tid & 63) == 0) {
-        smax[tid >> 6] = mx;
-        snan[tid >> 6] = nan;
-    }
-    if (tid == 0) sidx = 0x7FFFFFFF;
-    __syncthreads();
+    __shared__ float smax[4];
+    __shared__ bool snan[4];
+    __shared__ int sidx[4];
+    __shared__ double ssum[4];
+    if (WAVES > 1) {
+        if (lane == 0) {
+            smax[wave] = mx;
+            snan[wave] = nan;
+        }
+        __syncthreads();
 #pragma unroll
-    for (int v = 0; v < kVThreads / 64; ++v) {
-        mx = fmaxf(mx, smax[v]);
-        nan |= snan[v];
+        for (int v = 0; v < WAVES; ++v) {
+            mx = fmaxf(mx, smax[v]);
+            nan |= snan[v];
+        }
     }
     // the first index that has the maximum
-    if (own == mx && mx > -INFINITY) {
-        int mi = 0x7FFFFFFF;
+    int mi = 0x7FFFFFFF;
+    if (own == mx && mx > -INFINITY)
 #pragma unroll
-        for (int g = PER / E - 1; g >= 0; --g)
+        for (int g = G - 1; g >= 0; --g)
 #pragma unroll
-            for (int j = E - 1; j >= 0; --j) mi = x[g][j] == mx ? c0 + (g * kVThreads + tid) * E + j : mi;
-        atomicMin(&sidx, mi);
-    }
+            for (int j = E - 1; j >= 0; --j) mi = x[g][j] == mx ? c0 + (g * T + tid) * E + j : mi;
+    for (int m = 1; m < 64; m <<= 1) mi = min(mi, __shfl_xor(mi, m, 64));
     double sum = 0.0;
     if (it > 0.0) {
         if (id >= c0 && id < c1) {
 #pragma unroll
-            for (int g = 0; g < PER / E; ++g)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int j = 0; j < E; ++j)
-                    if (c0 + (g * kVThreads + tid) * E + j == id) x[g][j] = -INFINITY;
+                    if (c0 + (g * T + tid) * E + j == id) x[g][j] = -INFINITY;
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
-        if (!EXACT) {
+        if (EXACT) {
+            // terms far below the maximum (and a NaN, which is noted) become 2^-1000,
+            // nothing beside its 1
+            const float low = (float)fmax((double)ref - 1000.0 / it, -3.0e38);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum += exp2_neg((double)fmaxf(x[g][j], low) - (double)ref, it);
+        } else {
             const float c = (float)it;
             float part = 0.0f;
 #pragma unroll
-            for (int g = 0; g < PER / E; ++g)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f((x[g][j] - ref) * c);
             sum = part;
-        } else {
-        // terms far below the maximum (and a NaN, which is noted) become 2^-1000,
-        // nothing beside its 1
-        const float low = (float)fmax((double)ref - 1000.0 / it, -3.0e38);
-#pragma unroll
-        for (int g = 0; g < PER / E; ++g)
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum += exp2_neg((double)fmaxf(x[g][j], low) - (double)ref, it);
         }
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
-        if ((tid & 63) == 0) ssum[tid >> 6] = sum;
     }
-    __syncthreads();
+    if (WAVES > 1) {
+        if (lane == 0) {
+            ssum[wave] = sum;
+            sidx[wave] = mi;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) mi = min(mi, sidx[v]);
+        sum = 0.0;
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) sum += ssum[v];
+    }
     if (tid == 0) {
         VPart p;
-        p.sum = 0.0;
-        if (it > 0.0 && mx > -INFINITY)
-            for (int v = 0; v < kVThreads / 64; ++v) p.sum += ssum[v];
-        if (nan) p.sum = NAN;
+        p.sum = nan ? NAN : it > 0.0 && mx > -INFINITY ? sum : 0.0;
         p.max = mx;
-        p.idx = mx > -INFINITY ? sidx : -1;
+        p.idx = mx > -INFINITY ? mi : -1;
         a.part[((int64_t)(b * a.max_rows + i) * kinds + kind) * a.chunks + chunk] = p;
     }
 }
@@ -290,15 +304,11 @@ constexpr int kDecideThreads = 512;
 
 // The sum of a whole row in fp64, by the whole workgroup.
 template <bool BF16>
-__device__ __forceinline__ double row_sum(const VerifyArgs &a, int64_t row, float max, double it, bool vec) {
+__device__ __forceinline__ double row_sum(const VerifyArgs &a, int64_t row, float max, double it) {
     __shared__ double part[kDecideThreads / 64];
     double sum = 0.0;
-    for (int e0 = threadIdx.x * 8; e0 < a.vocab; e0 += kDecideThreads * 8) {
-        float x[8];
-        load_logits<BF16, 8>(a.logits, row * a.stride, e0, a.vocab, vec, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += term(x[i], max, it);
-    }
+#pragma unroll 4
+    for (int e = threadIdx.x; e < a.vocab; e += kDecideThreads) sum += term(logit<BF16>(a.logits, row * a.stride + e), max, it);
     for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
@@ -313,7 +323,7 @@ __device__ __forceinline__ double row_sum(const VerifyArgs &a, int64_t row, floa
 // wq; with fp32 sums a test whose sides agree to 2^-16 is made again with the row's
 // fp64 sum.
 template <bool BF16>
-__device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q, double it, int kinds, bool vec, Decision &d) {
+__device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q, double it, int kinds, Decision &d) {
     __shared__ VRow sp[kMaxRows], sq[kMaxRows];
     __shared__ double swd[kMaxRows];
     __shared__ float sua[kMaxRows];
@@ -363,7 +373,7 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
     int at = 0;
     for (;; ++at) {                                   // the last row always stops
         int stop = sstop[at];
-        if (stop == 2) stop = !((double)sua[at] * row_sum<BF16>(a, q.r0 + at, sp[at].max, it, vec) < swd[at]);
+        if (stop == 2) stop = !((double)sua[at] * row_sum<BF16>(a, q.r0 + at, sp[at].max, it) < swd[at]);
         if (stop) break;
     }
     const bool last = at == q.n - 1;
@@ -407,32 +417,37 @@ __device__ __forceinline__ void weights(const VerifyArgs &a, const Decision &d, 
     }
 }
 
-// The decisions, and per chunk the fp64 sums of what is drawn from: max(p - q, 0),
-// or p, or p without the draft.
-template <bool BF16, int PER>
-__global__ __launch_bounds__(kDecideThreads) void k_verify_rest(VerifyArgs a, int kinds, bool vec) {
-    constexpr int N = PER * kVThreads / kDecideThreads;
-    const int chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks;
+template <bool BF16>
+__global__ __launch_bounds__(kDecideThreads) void k_verify_decide(VerifyArgs a, int kinds) {
+    const int b = blockIdx.x;
     const VSeq q = verify_seq(a, b);
     if (q.n == 0) return;
-    const double it = inv_temp(a, b);
     Decision d;
-    decide<BF16>(a, b, q, it, kinds, vec, d);
-    if (chunk == 0 && threadIdx.x == 0) a.decided[b] = d;
+    decide<BF16>(a, b, q, inv_temp(a, b), kinds, d);
+    if (threadIdx.x == 0) a.decided[b] = d;
+}
+
+// Per chunk (a wavefront, four steps of 512 elements) the fp64 sums of what is drawn
+// from: max(p - q, 0), or p, or p without the draft.
+template <bool BF16>
+__global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool vec) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, blocks = (a.chunks + 3) / 4;
+    const int b = blockIdx.x / blocks, chunk = (blockIdx.x - b * blocks) * 4 + wave;
+    const VSeq q = verify_seq(a, b);
+    if (q.n == 0 || chunk >= a.chunks) return;
+    const Decision d = a.decided[b];
     if (d.mode == kGreedy) return;
-    const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
-    double w[N], sum = 0.0;
-    weights<BF16, N>(a, d, d.mode, q.r0 + d.row, c0 + (int)threadIdx.x * N, c1, it, vec, w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum += w[i];
-    for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
-    __shared__ double ssum[kDecideThreads / 64];
-    if ((threadIdx.x & 63) == 0) ssum[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kDecideThreads / 64; ++i) sum += ssum[i];
-        a.rest[(int64_t)b * a.chunks + chunk] = sum;
+    const double it = inv_temp(a, b);
+    const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab);
+    double sum = 0.0;
+#pragma unroll 2
+    for (int k = 0; k < 4; ++k) {
+        double w[8];
+        weights<BF16, 8>(a, d, d.mode, q.r0 + d.row, c0 + k * 512 + lane * 8, c1, it, vec, w);
+        sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
     }
+    for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
+    if (lane == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum;
 }
 
 __device__ __forceinline__ double lane_f64(double v, int l) {
@@ -442,9 +457,9 @@ __device__ __forceinline__ double lane_f64(double v, int l) {
 }
 
 // One workgroup per sequence: the decision, the draw, the outputs.
-template <bool BF16, int PER>
+template <bool BF16, bool SECOND>
 __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, int kinds, bool vec) {
-    constexpr int N = PER * kVThreads / kDecideThreads;
+    constexpr int N = kChunk / kDecideThreads;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const VSeq q = verify_seq(a, b);
     if (q.n == 0) {
@@ -457,11 +472,11 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
     }
     const double it = inv_temp(a, b);
     Decision d;
-    if (a.second)
+    if (SECOND)
         d = a.decided[b];
     else
-        decide<BF16>(a, b, q, it, kinds, vec, d);
-    __shared__ int schunk, smode, first_hit, last_live;
+        decide<BF16>(a, b, q, it, kinds, d);
+    __shared__ int schunk, smode, shit[kDecideThreads / 64], slast[kDecideThreads / 64];
     __shared__ double starget, wsum[kDecideThreads / 64];
     int token = d.best;
     if (d.mode != kGreedy) {
@@ -471,7 +486,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
             // chunk weights, their running sum, and the chunk that passes u * total
             // (the partials of outright drafts are already without the draft)
             int mode = d.mode;
-            bool again = a.second;
+            bool again = SECOND;
             auto chunk_weight = [&](int c) {
                 if (c >= a.chunks) return 0.0;
                 if (again) return rest[c];
@@ -516,8 +531,6 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
                 schunk = hit;
                 starget = target - from;
                 smode = mode;
-                first_hit = 0x7FFFFFFF;
-                last_live = -1;
             }
         }
         __syncthreads();
@@ -525,7 +538,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
         if (chunk >= 0) {
             // the chunk again: N elements a thread, their running sum
             const double target = starget;
-            const int c0 = chunk * a.chunk, c1 = min(c0 + a.chunk, a.vocab), e0 = c0 + tid * N;
+            const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab), e0 = c0 + tid * N;
             double w[N], own = 0.0;
             weights<BF16, N>(a, d, smode, q.r0 + d.row, e0, c1, it, vec, w);
             int last = -1;
@@ -543,18 +556,30 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
             __syncthreads();
             double sum = run - own;
             for (int i = 0; i < wave; ++i) sum += wsum[i];
-            if (last >= 0) atomicMax(&last_live, last);
+            int at = -1;                              // the first element that passes the target
             if (sum + own > target && own > 0.0) {
-                int at = 0x7FFFFFFF;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     sum += w[i];
-                    at = min(at, w[i] > 0.0 && sum > target ? e0 + i : 0x7FFFFFFF);
+                    at = at < 0 && w[i] > 0.0 && sum > target ? e0 + i : at;
                 }
-                if (at != 0x7FFFFFFF) atomicMin(&first_hit, at);
+            }
+            // of the lowest lane that has one; the last element with weight of the
+            // highest lane
+            const uint64_t hits = __ballot(at >= 0), live = __ballot(last >= 0);
+            const int hit = hits ? __shfl(at, __builtin_ctzll(hits), 64) : -1;
+            const int end = live ? __shfl(last, 63 - __builtin_clzll(live), 64) : -1;
+            if (lane == 0) {
+                shit[wave] = hit;
+                slast[wave] = end;
             }
             __syncthreads();
-            token = first_hit != 0x7FFFFFFF ? first_hit : (last_live >= 0 ? last_live : d.best);
+            int fall = -1, found = -1;
+            for (int i = 0; i < kDecideThreads / 64; ++i) {
+                found = found < 0 ? shit[i] : found;
+                fall = slast[i] >= 0 ? slast[i] : fall;
+            }
+            token = found >= 0 ? found : (fall >= 0 ? fall : d.best);
         }
     }
     for (int i = tid; i < q.n; i += kDecideThreads)
@@ -567,52 +592,46 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
 }
 
 struct VerifyPlan {
-    int per, chunk, chunks;
-    bool exact, second;
+    int chunks;
+    bool exact, second, many;
     size_t part, ws;
 };
 
-// Elements a chunk: the largest of 1024..8192 that still gives the device four
-// workgroups a CU.
 static VerifyPlan verify_plan(int batch, int max_rows, int vocab, bool draft) {
     VerifyPlan p;
-    const int64_t rows = (int64_t)batch * max_rows;
-    p.per = 32;
-    while (p.per > 8 && rows * ((vocab + kVThreads * p.per - 1) / (kVThreads * p.per)) < (int64_t)num_cus() * 4) p.per /= 2;
-    p.chunk = kVThreads * p.per;
-    p.chunks = (vocab + p.chunk - 1) / p.chunk;
-    p.part = (size_t)rows * (draft ? 2 : 1) * p.chunks * sizeof(VPart);
-    // Outright drafts: fp32 partials and a second pass over the drawn rows once
-    // the chunks fill the device several times over (337 rows of 151936: 69 us with
-    // fp64 partials of every row), fp64 partials and no second pass below (4 rows:
-    // 15.7 us).
-    p.exact = draft || p.per < 32;
+    const int64_t rows = (int64_t)batch * max_rows * (draft ? 2 : 1);
+    p.chunks = (vocab + kChunk - 1) / kChunk;
+    // a wavefront a chunk once they fill the device's SIMDs four deep
+    p.many = rows * p.chunks >= (int64_t)num_cus() * 16;
+    // Outright drafts of many rows: fp32 partials and a second pass over the drawn
+    // rows (337 rows of 151936: 63 us against 68 with fp64 partials of every row); of
+    // few: fp64 partials, no second pass (4 rows: 15.7 us with two launches).
+    p.exact = draft || !p.many;
     p.second = draft || !p.exact;
+    p.part = (size_t)rows * p.chunks * sizeof(VPart);
     p.ws = p.part + (p.second ? (size_t)batch * (p.chunks * sizeof(double) + sizeof(Decision)) : 0);
     return p;
 }
 
-template <bool BF16, int PER>
-static void launch_verify(const VerifyArgs &a, bool draft, bool vec, hipStream_t s) {
-    const int kinds = draft ? 2 : 1;
-    const unsigned grid = (unsigned)((int64_t)a.batch * a.max_rows * kinds * a.chunks);
-    if (a.exact)
-        hipLaunchKernelGGL((k_verify_stats<BF16, PER, true>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
-    else if constexpr (PER == 32)
-        hipLaunchKernelGGL((k_verify_stats<BF16, PER, false>), dim3(grid), dim3(kVThreads), 0, s, a, kinds, vec);
-    if (a.second)
-        hipLaunchKernelGGL((k_verify_rest<BF16, PER>), dim3((unsigned)(a.batch * a.chunks)), dim3(kDecideThreads), 0, s, a, kinds,
-                           vec);
-    hipLaunchKernelGGL((k_verify_pick<BF16, PER>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
-}
-
 template <bool BF16>
-static void launch_verify(const VerifyArgs &a, int per, bool draft, bool vec, hipStream_t s) {
-    switch (per) {
-        case 8: launch_verify<BF16, 8>(a, draft, vec, s); break;
-        case 16: launch_verify<BF16, 16>(a, draft, vec, s); break;
-        default: launch_verify<BF16, 32>(a, draft, vec, s); break;
+static void launch_verify(const VerifyArgs &a, bool many, bool draft, bool vec, hipStream_t s) {
+    const int kinds = draft ? 2 : 1;
+    const int64_t rows = (int64_t)a.batch * a.max_rows * kinds;
+    const dim3 grid((unsigned)(rows * (many ? (a.chunks + 3) / 4 : a.chunks)));
+    if (!many)
+        hipLaunchKernelGGL((k_verify_stats<BF16, 4, true>), grid, dim3(kVThreads), 0, s, a, kinds, vec);
+    else if (a.exact)
+        hipLaunchKernelGGL((k_verify_stats<BF16, 1, true>), grid, dim3(kVThreads), 0, s, a, kinds, vec);
+    else
+        hipLaunchKernelGGL((k_verify_stats<BF16, 1, false>), grid, dim3(kVThreads), 0, s, a, kinds, vec);
+    if (a.second) {
+        hipLaunchKernelGGL((k_verify_decide<BF16>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds);
+        hipLaunchKernelGGL((k_verify_rest<BF16>), dim3((unsigned)(a.batch * ((a.chunks + 3) / 4))), dim3(kVThreads), 0, s, a, vec);
     }
+    if (a.second)
+        hipLaunchKernelGGL((k_verify_pick<BF16, true>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
+    else
+        hipLaunchKernelGGL((k_verify_pick<BF16, false>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
 }
 
 }  // namespace nvfp4
@@ -682,7 +701,6 @@ extern "C" int verify_drafts(const void *logits, int32_t logits_dtype, int64_t r
     a.tokens = out_tokens;
     a.next = out_next;
     a.out_lens = out_kv_lens;
-    a.chunk = p.chunk;
     a.chunks = p.chunks;
     a.exact = p.exact;
     a.second = p.second;
@@ -693,8 +711,8 @@ extern "C" int verify_drafts(const void *logits, int32_t logits_dtype, int64_t r
                      (!draft_logits || (aligned(draft_logits, 16) && draft_stride * el % 16 == 0));
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (bf16)
-        launch_verify<true>(a, p.per, draft_logits != nullptr, vec, s);
+        launch_verify<true>(a, p.many, draft_logits != nullptr, vec, s);
     else
-        launch_verify<false>(a, p.per, draft_logits != nullptr, vec, s);
+        launch_verify<false>(a, p.many, draft_logits != nullptr, vec, s);
     return check_launch(who);
 }
