@@ -62,6 +62,12 @@ __device__ __forceinline__ double exp2_neg(double d, double c) {
     const uint32_t hi = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)u);
 }
+// The lowest logit whose term is taken as it is: terms far below the maximum (and
+// NaN) become 2^-1000, nothing beside the maximum's 1.
+__device__ __forceinline__ float lowest(float max, double c) { return (float)fmax((double)max - 1000.0 / c, -3.0e38); }
+__device__ __forceinline__ double term_above(float l, float max, float low, double c) {
+    return exp2_neg((double)fmaxf(l, low) - (double)max, c);
+}
 // exp((l - max) / T), c = log2(e) / T: 0 far below the maximum (and for l =
 // -inf), NaN for NaN.
 __device__ __forceinline__ double term(float l, float max, double c) {
@@ -229,13 +235,11 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
         if (EXACT) {
-            // terms far below the maximum (and a NaN, which is noted) become 2^-1000,
-            // nothing beside its 1
-            const float low = (float)fmax((double)ref - 1000.0 / it, -3.0e38);
+            const float low = lowest(ref, it);        // (a NaN is noted)
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int j = 0; j < E; ++j) sum += exp2_neg((double)fmaxf(x[g][j], low) - (double)ref, it);
+                for (int j = 0; j < E; ++j) sum += term_above(x[g][j], ref, low, it);
         } else {
             const float c = (float)it;
             float part = 0.0f;
@@ -439,15 +443,32 @@ __global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool ve
     if (d.mode == kGreedy) return;
     const double it = inv_temp(a, b);
     const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab);
+    const int64_t row = q.r0 + d.row;
+    const float plow = lowest(d.pmax, it), qlow = d.mode == kRest ? lowest(d.qmax, it) : 0.0f;
+    const double ip = 1.0 / d.psum, iq = 1.0 / d.qsum;
     double sum = 0.0;
 #pragma unroll 2
     for (int k = 0; k < 4; ++k) {
-        double w[8];
-        weights<BF16, 8>(a, d, d.mode, q.r0 + d.row, c0 + k * 512 + lane * 8, c1, it, vec, w);
-        sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        const int e0 = c0 + k * 512 + lane * 8;
+        float x[8];
+        load_logits<BF16, 8>(a.logits, row * a.stride, e0, c1, vec, x);
+        if (d.mode == kRest) {
+            float y[8];
+            load_logits<BF16, 8>(a.draft, row * a.dstride, e0, c1, vec, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double r = term_above(x[i], d.pmax, plow, it) * ip - term_above(y[i], d.qmax, qlow, it) * iq;
+                sum += r > 0.0 ? r : 0.0;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum += term_above(d.mode == kWithout && e0 + i == d.draft ? -INFINITY : x[i], d.pmax, plow, it);
+        }
     }
     for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
-    if (lane == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum;
+    // a chunk of nothing but terms far below holds no weight
+    if (lane == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum > 0x1p-900 ? sum : 0.0;
 }
 
 __device__ __forceinline__ double lane_f64(double v, int l) {
