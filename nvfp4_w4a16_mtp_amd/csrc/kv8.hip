@@ -15,9 +15,13 @@
 // Append.  One workgroup owns one (page, head) of K or of V: the scale of a
 // page needs the maximum over every token the call writes to it, and a grown
 // scale re-rounds the page's older codes, so no two workgroups may share a
-// page.  The rows stay in registers between the maximum and the encoding.  A
-// thread's unit is a cell of 4 tokens x 8 elements: 16-byte loads, 8-byte K
-// stores, and dword V stores of 4 tokens (V is transposed in its page).
+// page.  A thread's unit is a cell of 4 tokens x 8 elements: 16-byte loads, 8-byte
+// K stores, and dword V stores of 4 tokens (V is transposed in its page).  The
+// workgroup has a thread for every cell of the page (64 to 1024), so the rows stay
+// in registers between the maximum and the encoding.  Rotated k elements pass
+// through LDS, each pair turned once (turned where a cell needs them, the code of
+// the unrolled angles, 50 to 180 KB, took longer to fetch than to run: 14 us
+// instead of 8 for 64 sequences of 1 to 4 rows).
 #include "kv8.hpp"
 
 namespace nvfp4 {
@@ -83,6 +87,14 @@ struct Turn8 {
             py[i] = pack_bf16(x0 * s[2 * i] + y0 * c[2 * i], x1 * s[2 * i + 1] + y1 * c[2 * i + 1]);
         }
     }
+    __device__ __forceinline__ void apply(uint4 &x, uint4 &y, bool inter) const {
+        if (inter) {
+            apply_inter<0>(x);
+            apply_inter<4>(y);
+        } else {
+            apply_half(x, y);
+        }
+    }
     // pairs OFF .. OFF + 3 on one octet
     template <int OFF>
     __device__ __forceinline__ void apply_inter(uint4 &x) const {
@@ -121,12 +133,7 @@ __device__ __forceinline__ void rope_unit(const RopeTask &t, const Rope &rp, int
     for (int h = h0; h < h1; ++h) {
         uint4 x = *reinterpret_cast<const uint4 *>(src + h * t.in.head + d0);
         uint4 y = *reinterpret_cast<const uint4 *>(src + h * t.in.head + d1);
-        if (rp.inter) {
-            w.apply_inter<0>(x);
-            w.apply_inter<4>(y);
-        } else {
-            w.apply_half(x, y);
-        }
+        w.apply(x, y, rp.inter);
         *reinterpret_cast<uint4 *>(dst + h * t.out.head + d0) = x;
         *reinterpret_cast<uint4 *>(dst + h * t.out.head + d1) = y;
     }
@@ -154,6 +161,13 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t into, float a, float b) {
     a = a > 448.0f ? 448.0f : (a < -448.0f ? -448.0f : a);
     b = b > 448.0f ? 448.0f : (b < -448.0f ? -448.0f : b);
     return __builtin_amdgcn_cvt_pk_fp8_f32(a, b, into, HI);
+}
+// Two packed bf16 pairs times 2^-e -> four codes.
+__device__ __forceinline__ uint32_t encode4(uint32_t lo, uint32_t hi, int e) {
+    const uint32_t v = e4m3_pair<false>(0u, __builtin_ldexpf(bf16_bits_to_f32(lo & 0xFFFFu), -e),
+                                        __builtin_ldexpf(bf16_bits_to_f32(lo >> 16), -e));
+    return e4m3_pair<true>(v, __builtin_ldexpf(bf16_bits_to_f32(hi & 0xFFFFu), -e),
+                           __builtin_ldexpf(bf16_bits_to_f32(hi >> 16), -e));
 }
 // Four codes re-rounded to a scale 2^up times as large.
 __device__ __forceinline__ uint32_t requant4(uint32_t w, int up) {
@@ -189,38 +203,15 @@ __device__ __forceinline__ int scale_exp(uint32_t bits) {
     return max(e, kMinExp);
 }
 
-// The octet at element d of k row `src` at position pos, rotated.
-__device__ __forceinline__ uint4 rope_octet(const uint16_t *src, int d, const Rope &rp, double pos) {
-    uint4 x = *reinterpret_cast<const uint4 *>(src + d);
-    if (d >= rp.rot) return x;
-    Turn8 w;
-    if (rp.inter) {
-        // four pairs; the other four angles are not used and fall away
-        const int i0 = (d >> 4) * 8;
-        w.load(rp, pos, i0);
-        if (d & 8) w.apply_inter<4>(x); else w.apply_inter<0>(x);
-        return x;
-    }
-    const int half = rp.rot >> 1;
-    const bool lo = d < half;
-    w.load(rp, pos, lo ? d : d - half);
-    uint4 y = *reinterpret_cast<const uint4 *>(src + (lo ? d + half : d - half));
-    if (lo) {
-        w.apply_half(x, y);
-        return x;
-    }
-    w.apply_half(y, x);
-    return x;
-}
-
-// NC cells a thread.
-template <int NC>
-__global__ __launch_bounds__(256) void k_append(AppendArgs a) {
-    const int bid = blockIdx.x, tid = threadIdx.x;
-    if (bid >= a.kv_blocks) {
+// ROPE: the k rows are rotated (dynamic LDS: page_tokens * rot bf16).
+template <bool ROPE>
+__global__ __launch_bounds__(1024) void k_append(AppendArgs a) {
+    extern __shared__ uint4 turned[];                 // [token of the page][rot / 8]
+    const int bid = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
+    if (ROPE && bid >= a.kv_blocks) {
         // q rows: thread = (unit, row of the sequence, sequence)
         const int qb = bid - a.kv_blocks, group = qb % a.q_groups;
-        const int64_t i = (int64_t)(qb / a.q_groups) * 256 + tid;
+        const int64_t i = (int64_t)(qb / a.q_groups) * threads + tid;
         const int64_t r = i / a.q_units;
         const int b = (int)(r / a.s.max_rows), j = (int)(r % a.s.max_rows);
         if (b >= a.s.batch) return;
@@ -243,107 +234,111 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     if (end <= 0 || (int64_t)idx << a.c.lp >= end) return;
     const int page = a.s.table[(int64_t)b * a.s.max_pages + idx];
     if (page < 0 || page >= a.c.pages) return;
+    uint8_t *scale = (is_v ? a.c.vs : a.c.ks) + (int64_t)page * a.c.heads + h;
+    const int e_old = kv8_exp(*scale);
     const int p0 = idx << a.c.lp;
     const int o0 = max(start - p0, 0), o1 = min(end - p0, P);
     const int oct = a.dim >> 3;
     const HeadRows &in = is_v ? a.vin : a.kin;
     // row of token p0: rows run with the positions
     const uint16_t *src = in.data + ((int64_t)sq.r0 + p0 - shift) * in.row + h * in.head;
-
+    const bool rotate = ROPE && !is_v;
+    const int turns = rotate ? a.rp.rot >> 4 : 0;     // units of 8 pairs
+    if (rotate) {
+        for (int i = tid; i < (o1 - o0) * turns; i += threads) {
+            const int t = o0 + i / turns, u = i % turns;
+            const int d0 = a.rp.inter ? u * 2 : u, d1 = a.rp.inter ? d0 + 1 : d0 + turns;   // octets
+            const uint4 *row = reinterpret_cast<const uint4 *>(src + (int64_t)t * in.row);
+            uint4 x = row[d0], y = row[d1];
+            Turn8 turn;
+            turn.load(a.rp, (double)(p0 + t), u * 8);
+            turn.apply(x, y, a.rp.inter);
+            turned[t * 2 * turns + d0] = x;
+            turned[t * 2 * turns + d1] = y;
+        }
+        __syncthreads();
+    }
     // cells: K octet fastest (row loads and stores run along the row); V quad
     // fastest (its stores run along the tokens)
-    const int quads = P >> 2, cells = quads * oct;
-    uint4 x[NC][4];
+    const int quads = P >> 2;
+    const int quad = is_v ? tid & (quads - 1) : tid / oct, o = is_v ? tid >> (a.c.lp - 2) : tid - quad * oct;
+    const int t0 = quad * 4;
+    const bool cell = o < oct && quad < quads;
+    uint4 x[4];
     uint32_t mx = 0;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int cell = c * 256 + tid;
-        const int quad = is_v ? cell & (quads - 1) : cell / oct, o = is_v ? cell >> (a.c.lp - 2) : cell % oct;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = quad * 4 + j;
-            x[c][j] = make_uint4(0, 0, 0, 0);
-            if (cell < cells && t >= o0 && t < o1) {
-                const uint16_t *row = src + (int64_t)t * in.row;
-                x[c][j] = !is_v && a.rp.rot > 0 ? rope_octet(row, o * 8, a.rp, (double)(p0 + t))
-                                                : *reinterpret_cast<const uint4 *>(row + o * 8);
-            }
-        }
+    for (int j = 0; j < 4; ++j) {
+        const int t = t0 + j;
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (cell && t >= o0 && t < o1)
+            x[j] = o < 2 * turns ? turned[t * 2 * turns + o] : reinterpret_cast<const uint4 *>(src + (int64_t)t * in.row)[o];
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            mx = finite_max(mx, x[c][j].x);
-            mx = finite_max(mx, x[c][j].y);
-            mx = finite_max(mx, x[c][j].z);
-            mx = finite_max(mx, x[c][j].w);
-        }
-    uint8_t *scale = (is_v ? a.c.vs : a.c.ks) + (int64_t)page * a.c.heads + h;
-    const int e_old = kv8_exp(*scale);
-    __shared__ uint32_t wmax[4];
+    for (int j = 0; j < 4; ++j) {
+        mx = finite_max(mx, x[j].x);
+        mx = finite_max(mx, x[j].y);
+        mx = finite_max(mx, x[j].z);
+        mx = finite_max(mx, x[j].w);
+    }
+    __shared__ uint32_t wmax[16];
     for (int off = 32; off > 0; off >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
     if ((tid & 63) == 0) wmax[tid >> 6] = mx;
     __syncthreads();                                  // every thread has read the old scale
-    int e = scale_exp(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+    for (int i = 0; i < threads >> 6; ++i) mx = max(mx, wmax[i]);
+    int e = scale_exp(mx);
     const bool older = o0 > 0;
     if (older) e = max(e, e_old);
     const int up = older ? e - e_old : 0;
     if (tid == 0) *scale = (uint8_t)(e + 127);
+    if (!cell || t0 >= o1 || (t0 + 4 <= o0 && up == 0)) return;
     uint8_t *dst = (is_v ? a.c.v : a.c.k) + ((int64_t)page * a.c.heads + h) * ((int64_t)a.dim << a.c.lp);
+    uint32_t code[4][2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int cell = c * 256 + tid;
-        const int quad = is_v ? cell & (quads - 1) : cell / oct, o = is_v ? cell >> (a.c.lp - 2) : cell % oct;
-        const int t0 = quad * 4;
-        if (cell >= cells || t0 >= o1 || (t0 + 4 <= o0 && up == 0)) continue;
-        uint32_t code[4][2];
+    for (int j = 0; j < 4; ++j) {
+        code[j][0] = encode4(x[j].x, x[j].y, e);
+        code[j][1] = encode4(x[j].z, x[j].w, e);
+    }
+    if (!is_v) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t p[4] = {x[c][j].x, x[c][j].y, x[c][j].z, x[c][j].w};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t lo = p[2 * q], hi = p[2 * q + 1];
-                uint32_t v = e4m3_pair<false>(0u, __builtin_ldexpf(bf16_bits_to_f32(lo & 0xFFFFu), -e),
-                                              __builtin_ldexpf(bf16_bits_to_f32(lo >> 16), -e));
-                code[j][q] = e4m3_pair<true>(v, __builtin_ldexpf(bf16_bits_to_f32(hi & 0xFFFFu), -e),
-                                             __builtin_ldexpf(bf16_bits_to_f32(hi >> 16), -e));
+            const int t = t0 + j;
+            uint2 *at = reinterpret_cast<uint2 *>(dst + (int64_t)t * a.dim + o * 8);
+            if (t >= o0 && t < o1) {
+                *at = make_uint2(code[j][0], code[j][1]);
+            } else if (t < o0 && up > 0) {
+                const uint2 old = *at;
+                *at = make_uint2(requant4(old.x, up), requant4(old.y, up));
             }
         }
-        if (!is_v) {
+        return;
+    }
+    // V: element d of the four tokens is one dword; merged with what the page holds
+    // where only some of them are new
+    uint32_t fresh = 0, held = 0;                     // bytes that are new, and that hold older tokens
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + j;
-                uint2 *at = reinterpret_cast<uint2 *>(dst + (int64_t)t * a.dim + o * 8);
-                if (t >= o0 && t < o1) {
-                    *at = make_uint2(code[j][0], code[j][1]);
-                } else if (t < o0 && up > 0) {
-                    const uint2 old = *at;
-                    *at = make_uint2(requant4(old.x, up), requant4(old.y, up));
-                }
-            }
-        } else {
-            // bytes of the quad that are new, and those that hold older tokens
-            uint32_t fresh = 0, held = 0;
+    for (int j = 0; j < 4; ++j) {
+        fresh |= (t0 + j >= o0 && t0 + j < o1) ? 0xFFu << (8 * j) : 0u;
+        held |= (t0 + j < o0) ? 0xFFu << (8 * j) : 0u;
+    }
+    uint32_t *at = reinterpret_cast<uint32_t *>(dst + (((int64_t)o * 8) << a.c.lp) + t0);
+    const int step = P >> 2;                          // dwords from one dim to the next
+    uint32_t old[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                fresh |= (t0 + j >= o0 && t0 + j < o1) ? 0xFFu << (8 * j) : 0u;
-                held |= (t0 + j < o0) ? 0xFFu << (8 * j) : 0u;
-            }
+    for (int d = 0; d < 8; ++d) old[d] = fresh != 0xFFFFFFFFu ? at[d * step] : 0u;
+    if (up > 0) {
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                uint32_t *at = reinterpret_cast<uint32_t *>(dst + (((int64_t)o * 8 + d) << a.c.lp) + t0);
-                uint32_t v = 0;
+        for (int d = 0; d < 8; ++d) old[d] = (requant4(old[d], up) & held) | (old[d] & ~held);
+    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v |= ((code[j][d >> 2] >> (8 * (d & 3))) & 0xFFu) << (8 * j);
-                if (fresh != 0xFFFFFFFFu) {
-                    const uint32_t old = *at;
-                    const uint32_t kept = up > 0 ? requant4(old, up) : old;
-                    v = (v & fresh) | (kept & held) | (old & ~(fresh | held));
-                }
-                *at = v;
-            }
-        }
+    for (int h2 = 0; h2 < 2; ++h2) {
+        // 4 x 4 bytes transposed: two rounds of byte merges
+        const uint32_t a0 = code[0][h2], a1 = code[1][h2], a2 = code[2][h2], a3 = code[3][h2];
+        const uint32_t lo01 = __builtin_amdgcn_perm(a1, a0, 0x05010400u), hi01 = __builtin_amdgcn_perm(a1, a0, 0x07030602u);
+        const uint32_t lo23 = __builtin_amdgcn_perm(a3, a2, 0x05010400u), hi23 = __builtin_amdgcn_perm(a3, a2, 0x07030602u);
+        const uint32_t v[4] = {__builtin_amdgcn_perm(lo23, lo01, 0x05040100u), __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
+                               __builtin_amdgcn_perm(hi23, hi01, 0x05040100u), __builtin_amdgcn_perm(hi23, hi01, 0x07060302u)};
+#pragma unroll
+        for (int d = 0; d < 4; ++d) at[(h2 * 4 + d) * step] = (v[d] & fresh) | (old[h2 * 4 + d] & ~fresh);
     }
 }
 
@@ -565,24 +560,25 @@ static int append(const char *who, const nvfp4_kv8_cache *cache, const nvfp4_kv8
     a.items = (int)(((int64_t)max_rows + 2 * P - 2) / P);
     const int64_t kv_blocks = (int64_t)seqs->batch * a.items * 2 * cache->kv_heads;
     a.q_units = a.q_per = a.q_groups = 1;
+    const int cells = P / 4 * (a.dim / 8);            // 32 .. 1024
+    const int threads = (cells + 63) / 64 * 64;
     int64_t blocks = kv_blocks;
     if (tq.heads > 0) {
         a.q_units = rope_units(tq, a.dim, a.rp.rot);
-        const int64_t threads = (int64_t)seqs->batch * max_rows * a.q_units;
-        a.q_per = heads_per_thread(threads, tq.heads);
+        const int64_t units = (int64_t)seqs->batch * max_rows * a.q_units;
+        a.q_per = heads_per_thread(units, tq.heads);
         a.q_groups = (tq.heads + a.q_per - 1) / a.q_per;
-        blocks += (threads + 255) / 256 * a.q_groups;
+        blocks += (units + threads - 1) / threads * a.q_groups;
     }
     if (blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     a.kv_blocks = (int)kv_blocks;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const int cells = P / 4 * (a.dim / 8);
-    if (cells <= 256)
-        hipLaunchKernelGGL(k_append<1>, dim3((unsigned)blocks), dim3(256), 0, s, a);
-    else if (cells <= 512)
-        hipLaunchKernelGGL(k_append<2>, dim3((unsigned)blocks), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_append<4>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    if (rope) {
+        const size_t lds = (size_t)P * a.rp.rot * 2;  // at most 64 KiB
+        hipLaunchKernelGGL(k_append<true>, dim3((unsigned)blocks), dim3(threads), lds, s, a);
+    } else {
+        hipLaunchKernelGGL(k_append<false>, dim3((unsigned)blocks), dim3(threads), 0, s, a);
+    }
     return check_launch(who);
 }
 
