@@ -649,17 +649,79 @@ def moe_layer_w4a16(x: torch.Tensor, router: NVFP4Weight, top_k: int, experts: N
 
 
 # ---- attention of the draft step over a paged 8-bit cache, and verification
+#
+# A decode step's kernels take a few microseconds, so these bindings keep the
+# host's part short: descriptors of a cache and a batch are made once, pointers
+# go to the library as integers, and the device is switched only when it is not
+# the current one.
 
-@dataclass
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(what: str, fn, index: int, *args):
+    """fn(*args, stream) on device `index` and its current stream."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        _check(rc, what)
+
+
+def _int32(t: torch.Tensor, name: str):
+    _dev(t, name)
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32")
+
+
+def _same_device(index: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: cuda:{index} and {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str) -> _HeadRows:
+    """Head rows of a bf16 [rows][heads][dim] tensor (unit stride in dim)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bf16 [rows][heads][dim]")
+    n, heads, dim = t.shape
+    row, head, unit = t.stride()
+    if unit != 1 and dim != 1:
+        raise ValueError(f"{name} must have unit stride in dim")
+    return _HeadRows(t.data_ptr(), row if n > 1 else heads * dim, head if heads > 1 else dim, heads, dim)
+
+
+@dataclass(frozen=True)
 class KV8Cache:
     """A paged 8-bit KV cache on the device: k_codes [pages, kv_heads,
     page_tokens, head_dim] and v_codes [pages, kv_heads, head_dim,
     page_tokens] uint8 (E4M3), k_scales and v_scales [pages, kv_heads] uint8
-    (byte b stands for 2^(b - 127))."""
+    (byte b stands for 2^(b - 127)).  The tensors keep their storage."""
     k_codes: torch.Tensor
     k_scales: torch.Tensor
     v_codes: torch.Tensor
     v_scales: torch.Tensor
+
+    def __post_init__(self):
+        if self.k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages][kv_heads][page_tokens][head_dim]")
+        pages, heads, tokens, dim = self.k_codes.shape
+        for t, shape, name in ((self.k_codes, (pages, heads, tokens, dim), "k_codes"),
+                               (self.v_codes, (pages, heads, dim, tokens), "v_codes"),
+                               (self.k_scales, (pages, heads), "k_scales"), (self.v_scales, (pages, heads), "v_scales")):
+            _dev(t, name)
+            if t.dtype is not torch.uint8 or t.shape != shape:
+                raise ValueError(f"{name} must be uint8 {list(shape)}")
+        index = self.k_codes.get_device()
+        _same_device(index, self.k_scales, self.v_codes, self.v_scales)
+        d = _KV8Cache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                      self.v_scales.data_ptr(), pages, tokens, heads, dim)
+        for name, v in (("index", index), ("kv_heads", heads), ("page_tokens", tokens), ("head_dim", dim), ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, v)
 
     @staticmethod
     def empty(num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 16, device="cuda") -> "KV8Cache":
@@ -668,81 +730,47 @@ class KV8Cache:
         return KV8Cache(u8(num_pages, kv_heads, page_tokens, head_dim), u8(num_pages, kv_heads),
                         u8(num_pages, kv_heads, head_dim, page_tokens), u8(num_pages, kv_heads))
 
-    @property
-    def kv_heads(self):
-        return self.k_codes.shape[1]
 
-    @property
-    def page_tokens(self):
-        return self.k_codes.shape[2]
-
-    @property
-    def head_dim(self):
-        return self.k_codes.shape[3]
-
-    def desc(self) -> _KV8Cache:
-        pages, heads, tokens, dim = self.k_codes.shape
-        for t, shape, name in ((self.k_codes, (pages, heads, tokens, dim), "k_codes"),
-                               (self.v_codes, (pages, heads, dim, tokens), "v_codes"),
-                               (self.k_scales, (pages, heads), "k_scales"), (self.v_scales, (pages, heads), "v_scales")):
-            _dev(t, name)
-            if t.dtype != torch.uint8 or t.shape != shape:
-                raise ValueError(f"{name} must be uint8 {list(shape)}")
-        _one_device(self.k_codes, k_scales=self.k_scales, v_codes=self.v_codes, v_scales=self.v_scales)
-        return _KV8Cache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
-                         self.v_scales.data_ptr(), pages, tokens, heads, dim)
-
-
-@dataclass
+@dataclass(frozen=True)
 class KV8Seqs:
     """A ragged batch over a KV8Cache: cu_rows [batch + 1], kv_lens [batch]
     (this call's rows included) and block_table [batch, max_pages] int32 on
     the device; max_rows bounds a sequence's rows, max_kv_len its length (0:
-    what the table holds)."""
+    what the table holds).  The tensors keep their storage; their values are
+    read on the device by every call."""
     cu_rows: torch.Tensor
     kv_lens: torch.Tensor
     block_table: torch.Tensor
     max_rows: int
     max_kv_len: int = 0
 
-    def desc(self, rows: int) -> _KV8Seqs:
+    def __post_init__(self):
         batch = self.kv_lens.numel()
         for t, name in ((self.cu_rows, "cu_rows"), (self.kv_lens, "kv_lens"), (self.block_table, "block_table")):
             _int32(t, name)
         if self.cu_rows.numel() != batch + 1 or self.block_table.dim() != 2 or self.block_table.shape[0] != batch:
             raise ValueError("need cu_rows [batch + 1], kv_lens [batch], block_table [batch][max_pages]")
-        return _KV8Seqs(self.cu_rows.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(), batch, rows,
-                        self.max_rows, self.block_table.shape[1], self.max_kv_len)
+        index = self.kv_lens.get_device()
+        _same_device(index, self.cu_rows, self.block_table)
+        object.__setattr__(self, "index", index)
+        object.__setattr__(self, "_refs", {})
 
-
-def _int32(t: torch.Tensor, name: str):
-    _dev(t, name)
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-
-
-def _one_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-
-
-def _rows(t: torch.Tensor, name: str) -> _HeadRows:
-    """Head rows of a bf16 [rows][heads][dim] tensor (unit stride in dim)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-        raise ValueError(f"{name} must be bf16 [rows][heads][dim] with unit stride in dim")
-    n, heads, dim = t.shape
-    row = t.stride(0) if n > 1 else heads * dim
-    return _HeadRows(t.data_ptr(), row, t.stride(1) if heads > 1 else dim, heads, dim)
+    def _ref(self, rows: int):
+        ref = self._refs.get(rows)
+        if ref is None:
+            d = _KV8Seqs(self.cu_rows.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(), self.kv_lens.numel(),
+                         rows, self.max_rows, self.block_table.shape[1], self.max_kv_len)
+            if len(self._refs) >= 64:
+                self._refs.clear()
+            ref = self._refs[rows] = ctypes.byref(d)
+        return ref
 
 
 def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, mscale: float) -> _Rope:
     _dev(inv_freq, "inv_freq")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a float64 vector (rope_frequencies)")
-    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), mscale)
+    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved, mscale)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -785,40 +813,37 @@ def rope_qk(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Ten
     (either may be None; rows and heads may be strided).  Returns (q_out,
     k_out); pass q_out=q to rotate in place."""
     _int32(positions, "positions")
-    rows = positions.numel()
-    descs, outs = [], []
+    rows, index = positions.numel(), positions.get_device()
+    refs, outs = [], []
     for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
         if x is None:
             if out is not None:
                 raise ValueError(f"{name}_out without {name}")
-            descs += [None, None]
+            refs += [None, None]
             outs.append(None)
             continue
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         if x.shape[0] != rows or out.shape != x.shape:
             raise ValueError(f"{name} and {name}_out must have {rows} rows and one shape")
-        _one_device(positions, **{name: x, name + "_out": out})
-        descs += [ctypes.byref(_rows(x, name)), ctypes.byref(_rows(out, name + "_out"))]
+        _same_device(index, x, out)
+        refs += [ctypes.byref(_rows(x, name)), ctypes.byref(_rows(out, name + "_out"))]
         outs.append(out)
-    _one_device(positions, inv_freq=inv_freq)
-    rp = _rope_desc(inv_freq, interleaved, mscale)
-    with torch.cuda.device(positions.device):
-        _check(lib().rope_qk(*descs, rows, _ptr(positions), ctypes.byref(rp), _stream(positions)), "rope_qk")
+    _same_device(index, inv_freq)
+    _run("rope_qk", lib().rope_qk, index, *refs, rows, positions.data_ptr(),
+         ctypes.byref(_rope_desc(inv_freq, interleaved, mscale)))
     return tuple(outs)
 
 
 def kv8_append(cache: KV8Cache, seqs: KV8Seqs, k: torch.Tensor, v: torch.Tensor):
     """Quantises k and v, bf16 [rows][kv_heads][head_dim], into the cache at
     the rows' positions."""
-    dk, dv = _rows(k, "k"), _rows(v, "v")
     if k.shape != v.shape:
         raise ValueError("k and v must have one shape")
-    _one_device(cache.k_codes, k=k, v=v, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows, block_table=seqs.block_table)
-    c, s = cache.desc(), seqs.desc(k.shape[0])
-    with torch.cuda.device(k.device):
-        _check(lib().kv8_append(ctypes.byref(c), ctypes.byref(s), ctypes.byref(dk), ctypes.byref(dv), _stream(k)),
-               "kv8_append")
+    index = cache.index
+    _same_device(index, k, v, seqs.kv_lens)
+    _run("kv8_append", lib().kv8_append, index, cache._ref, seqs._ref(k.shape[0]), ctypes.byref(_rows(k, "k")),
+         ctypes.byref(_rows(v, "v")))
 
 
 def rope_kv8_append(cache: KV8Cache, seqs: KV8Seqs, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -827,25 +852,21 @@ def rope_kv8_append(cache: KV8Cache, seqs: KV8Seqs, q: torch.Tensor | None, k: t
     """rope_qk of q and k at the rows' positions, then kv8_append of the
     rotated k and of v, in one launch.  Returns the rotated q (None without
     q); pass q_out=q to rotate in place."""
-    dk, dv = _rows(k, "k"), _rows(v, "v")
     if k.shape != v.shape:
         raise ValueError("k and v must have one shape")
-    dq = dqo = None
-    if q is None and q_out is not None:
-        raise ValueError("q_out without q")
+    index, dq, dqo = cache.index, None, None
     if q is not None:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if q.shape[0] != k.shape[0] or q_out.shape != q.shape:
             raise ValueError("q and q_out must have k's rows and one shape")
         dq, dqo = ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(q_out, "q_out"))
-    _one_device(cache.k_codes, q=q, q_out=q_out, k=k, v=v, inv_freq=inv_freq, kv_lens=seqs.kv_lens,
-                cu_rows=seqs.cu_rows, block_table=seqs.block_table)
-    rp = _rope_desc(inv_freq, interleaved, mscale)
-    c, s = cache.desc(), seqs.desc(k.shape[0])
-    with torch.cuda.device(k.device):
-        _check(lib().rope_kv8_append(ctypes.byref(c), ctypes.byref(s), ctypes.byref(rp), dq, dqo, ctypes.byref(dk),
-                                     ctypes.byref(dv), _stream(k)), "rope_kv8_append")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(index, q, q_out, k, v, inv_freq, seqs.kv_lens)
+    _run("rope_kv8_append", lib().rope_kv8_append, index, cache._ref, seqs._ref(k.shape[0]),
+         ctypes.byref(_rope_desc(inv_freq, interleaved, mscale)), dq, dqo, ctypes.byref(_rows(k, "k")),
+         ctypes.byref(_rows(v, "v")))
     return q_out
 
 
@@ -854,32 +875,27 @@ def kv8_read(cache: KV8Cache, seqs: KV8Seqs, rows: int | None = None, k_out: tor
     """The values of each sequence's last tokens (as many as it owns rows) in
     bf16 [rows][kv_heads][head_dim].  Give the outputs, or `rows` to have both
     allocated here.  Returns (k_out, v_out)."""
+    index = cache.index
     if k_out is None and v_out is None:
         if rows is None:
             raise ValueError("kv8_read needs rows, k_out or v_out")
         shape = (rows, cache.kv_heads, cache.head_dim)
         k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device) for _ in range(2))
-    some = k_out if k_out is not None else v_out
-    if rows is None:
-        rows = some.shape[0]
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.shape[0] != rows:
-            raise ValueError(f"{name} must have {rows} rows")
-    _one_device(cache.k_codes, k_out=k_out, v_out=v_out, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows,
-                block_table=seqs.block_table)
-    dk = ctypes.byref(_rows(k_out, "k_out")) if k_out is not None else None
-    dv = ctypes.byref(_rows(v_out, "v_out")) if v_out is not None else None
-    c, s = cache.desc(), seqs.desc(rows)
-    with torch.cuda.device(some.device):
-        _check(lib().kv8_read(ctypes.byref(c), ctypes.byref(s), dk, dv, _stream(some)), "kv8_read")
+    elif rows is None:
+        rows = (k_out if k_out is not None else v_out).shape[0]
+    if (k_out is not None and k_out.shape[0] != rows) or (v_out is not None and v_out.shape[0] != rows):
+        raise ValueError(f"outputs must have {rows} rows")
+    _same_device(index, k_out, v_out, seqs.kv_lens)
+    _run("kv8_read", lib().kv8_read, index, cache._ref, seqs._ref(rows),
+         ctypes.byref(_rows(k_out, "k_out")) if k_out is not None else None,
+         ctypes.byref(_rows(v_out, "v_out")) if v_out is not None else None)
     return k_out, v_out
 
 
 def kv8_attention_workspace(cache: KV8Cache, seqs: KV8Seqs, q_heads: int, rows: int) -> torch.Tensor:
     """Workspace for kv8_attention of `rows` rows (nothing to initialise)."""
-    c, s = cache.desc(), seqs.desc(rows)
-    with torch.cuda.device(cache.k_codes.device):
-        nbytes = lib().kv8_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(s), q_heads)
+    with torch.cuda.device(cache.index):
+        nbytes = lib().kv8_attention_workspace_bytes(cache._ref, seqs._ref(rows), q_heads)
     if nbytes == 0:
         raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.k_codes.device)
@@ -890,24 +906,19 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float 
     """Attention of q, bf16 [rows][q_heads][head_dim], over the cache (scale:
     head_dim^-0.5 by default).  out: bf16 [rows][q_heads][head_dim], heads
     contiguous."""
-    dq = _rows(q, "q")
+    dq, index = _rows(q, "q"), cache.index
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     do = _rows(out, "out")
-    if out.shape != q.shape or do.head_stride != q.shape[2]:
+    if out.shape != q.shape or do.head_stride != do.dim:
         raise ValueError("out must have q's shape and contiguous heads")
     if workspace is None:
-        workspace = kv8_attention_workspace(cache, seqs, q.shape[1], q.shape[0])
+        workspace = kv8_attention_workspace(cache, seqs, dq.heads, q.shape[0])
     _dev(workspace, "workspace")
-    _one_device(cache.k_codes, q=q, out=out, workspace=workspace, kv_lens=seqs.kv_lens, cu_rows=seqs.cu_rows,
-                block_table=seqs.block_table)
-    if scale is None:
-        scale = q.shape[2] ** -0.5
-    c, s = cache.desc(), seqs.desc(q.shape[0])
-    with torch.cuda.device(q.device):
-        _check(lib().kv8_attention(ctypes.byref(dq), ctypes.byref(c), ctypes.byref(s), scale, window, sinks, _ptr(out),
-                                   do.row_stride, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                   _stream(q)), "kv8_attention")
+    _same_device(index, q, out, workspace, seqs.kv_lens)
+    _run("kv8_attention", lib().kv8_attention, index, ctypes.byref(dq), cache._ref, seqs._ref(q.shape[0]),
+         dq.dim ** -0.5 if scale is None else scale, window, sinks, do.data, do.row_stride, workspace.data_ptr(),
+         workspace.nbytes)
     return out
 
 
@@ -930,6 +941,15 @@ def verify_workspace(max_rows: int, batch: int, vocab: int, device, sampled: boo
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _vector(t: torch.Tensor | None, dtype, n: int, index: int, name: str):
+    """The pointer of a contiguous device vector (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} on cuda:{index}")
+    return t.data_ptr()
+
+
 def verify_drafts(logits: torch.Tensor, cu_rows: torch.Tensor, draft_ids: torch.Tensor, u_accept: torch.Tensor,
                   u_sample: torch.Tensor, max_rows: int, temperature: torch.Tensor | None = None,
                   draft_logits: torch.Tensor | None = None, kv_lens: torch.Tensor | None = None,
@@ -939,47 +959,33 @@ def verify_drafts(logits: torch.Tensor, cu_rows: torch.Tensor, draft_ids: torch.
     owns rows cu_rows[b] .. cu_rows[b + 1]; draft_ids[r] is the draft after row
     r (a sequence's last row has none).  draft_logits: the rows the drafts were
     sampled from, or None for drafts chosen outright."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    index, i32, f32 = logits.get_device(), torch.int32, torch.float32
     rows, vocab = logits.shape
     batch = cu_rows.numel() - 1
-    for t, name in ((cu_rows, "cu_rows"), (draft_ids, "draft_ids"), (kv_lens, "kv_lens")):
-        if t is not None:
-            _int32(t, name)
-    for t, name, n in ((u_accept, "u_accept", rows), (u_sample, "u_sample", batch), (temperature, "temperature", batch)):
-        if t is None:
-            continue
-        _dev(t, name)
-        if t.dtype != torch.float32 or t.numel() != n:
-            raise ValueError(f"{name} must be float32 with {n} elements")
-    if draft_ids.numel() != rows or (kv_lens is not None and kv_lens.numel() != batch):
-        raise ValueError("need draft_ids [rows] and kv_lens [batch]")
+    strides = []
     for t, name in ((logits, "logits"), (draft_logits, "draft_logits")):
-        if t is not None and (not t.is_cuda or t.dtype != logits.dtype or t.shape != logits.shape or
-                              (t.stride(1) != 1 and vocab != 1)):
-            raise ValueError(f"{name} must be a device tensor of the logits' type and shape, unit column stride")
-    dev = logits.device
+        if t is None:
+            strides.append(0)
+            continue
+        if t.dtype is not logits.dtype or t.shape != logits.shape or t.get_device() != index or (t.stride(1) != 1 and vocab != 1):
+            raise ValueError(f"{name} must have the logits' type, shape and device and unit column stride")
+        strides.append(t.stride(0) if rows > 1 else vocab)
     if workspace is None:
-        workspace = verify_workspace(max_rows, batch, vocab, dev, sampled=draft_logits is not None)
+        workspace = verify_workspace(max_rows, batch, vocab, logits.device, sampled=draft_logits is not None)
     _dev(workspace, "workspace")
+    _same_device(index, workspace)
     if out is None:
-        out = Verified(torch.empty(batch, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.int32, device=dev),
-                       torch.empty(batch, dtype=torch.int32, device=dev),
-                       torch.empty(batch, dtype=torch.int32, device=dev) if kv_lens is not None else None)
-    for t, name, n in ((out.accepted, "accepted", batch), (out.tokens, "tokens", rows), (out.next, "next", batch),
-                       (out.kv_lens, "kv_lens", batch)):
-        if t is not None:
-            _int32(t, "out." + name)
-            if t.numel() != n:
-                raise ValueError(f"out.{name} must have {n} elements")
-    _one_device(logits, cu_rows=cu_rows, draft_ids=draft_ids, u_accept=u_accept, u_sample=u_sample,
-                temperature=temperature, draft_logits=draft_logits, kv_lens=kv_lens, workspace=workspace,
-                accepted=out.accepted, tokens=out.tokens, next=out.next, out_kv_lens=out.kv_lens)
-
-    def stride(t):
-        return 0 if t is None else (t.stride(0) if rows > 1 else vocab)
-    with torch.cuda.device(dev):
-        _check(lib().verify_drafts(_ptr(logits), _out_code(logits.dtype), stride(logits), vocab, _ptr(draft_logits),
-                                   stride(draft_logits), _ptr(cu_rows), batch, rows, max_rows, _ptr(draft_ids),
-                                   _ptr(temperature), _ptr(u_accept), _ptr(u_sample), _ptr(kv_lens), _ptr(out.accepted),
-                                   _ptr(out.tokens), _ptr(out.next), _ptr(out.kv_lens), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(logits)), "verify_drafts")
+        parts = torch.empty(rows + (2 if kv_lens is None else 3) * batch, dtype=i32, device=logits.device) \
+            .split_with_sizes([batch, rows, batch] + ([] if kv_lens is None else [batch]))
+        out = Verified(*parts, *([None] if kv_lens is None else []))
+    _run("verify_drafts", lib().verify_drafts, index, logits.data_ptr(), _out_code(logits.dtype), strides[0], vocab,
+         draft_logits.data_ptr() if draft_logits is not None else None, strides[1],
+         _vector(cu_rows, i32, batch + 1, index, "cu_rows"), batch, rows, max_rows,
+         _vector(draft_ids, i32, rows, index, "draft_ids"), _vector(temperature, f32, batch, index, "temperature"),
+         _vector(u_accept, f32, rows, index, "u_accept"), _vector(u_sample, f32, batch, index, "u_sample"),
+         _vector(kv_lens, i32, batch, index, "kv_lens"), _vector(out.accepted, i32, batch, index, "out.accepted"),
+         _vector(out.tokens, i32, rows, index, "out.tokens"), _vector(out.next, i32, batch, index, "out.next"),
+         _vector(out.kv_lens, i32, batch, index, "out.kv_lens"), workspace.data_ptr(), workspace.nbytes)
     return out
