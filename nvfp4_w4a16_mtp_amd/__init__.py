@@ -684,11 +684,10 @@ def _same_device(index: int, *tensors):
 
 def _rows(t: torch.Tensor, name: str) -> _HeadRows:
     """Head rows of a bf16 [rows][heads][dim] tensor (unit stride in dim)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3:
         raise ValueError(f"{name} must be bf16 [rows][heads][dim]")
-    n, heads, dim = t.shape
+    n, heads, dim = shape
     row, head, unit = t.stride()
     if unit != 1 and dim != 1:
         raise ValueError(f"{name} must have unit stride in dim")

@@ -110,12 +110,6 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t nan_ones(uint32_t w) { return (nan_bytes(w) >> 7) * 0x38u; }
 
-// The same value, computed anew where it is used.
-__device__ __forceinline__ uint32_t opaque(uint32_t v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 // The key range of one row tile as a list of steps: those of the sinks, then
 // those from the window's first token on.
 struct Keys {
@@ -391,7 +385,7 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
     }
     __syncthreads();
 
-    auto sees = [&](int t, int p) { return t <= p && (a.window == 0 || t > p - a.window || t < a.sinks); };
+    auto sees = [&](int t, int p) { return (t <= p) & ((a.window == 0) | (t > p - a.window) | (t < a.sinks)); };
     // (wavefront, row tile) maxima of the step's scores
     auto row_max = [&](const f32x4 (&s)[RT][2], int rt) {
         float mx = s[rt][0][0];
@@ -424,7 +418,7 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
         for (int v = v0; v < v1; ++v) {
             const int buf = (v - v0) & 1, cur = step;
             const bool kv_ok = __all(valid(id.k[0]) && valid(id.k[1]) && valid(id.v[0]) && valid(id.v[1]));
-            const bool k_ok[2] = {valid(id.k[0]), valid(id.k[1])}, v_ok[2] = {valid(id.v[0]), valid(id.v[1])};
+            const bool k_ok[2] = {valid(id.k[0]), valid(id.k[1])};
             const float fk[2] = {kv8_scale(sk[0]), kv8_scale(sk[1])};
             f32x4 s[RT][2];
 #pragma unroll
@@ -463,7 +457,7 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!(k_ok[j] && sees(t0 + 32 * wave + 16 * j + 4 * g + i, pos[rt]))) s[rt][j][i] = -INFINITY;
+                            s[rt][j][i] = k_ok[j] & sees(t0 + 32 * wave + 16 * j + 4 * g + i, pos[rt]) ? s[rt][j][i] : -INFINITY;
                 }
                 mx[rt] = row_max(s, rt);
                 need |= mx[rt] > m[rt] + kSlack;
@@ -510,37 +504,39 @@ __global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 1
                     for (int dt = 0; dt < DW; ++dt)
                         any |= nan_bytes(vf[j][dt].x) | nan_bytes(vf[j][dt].y) | nan_bytes(vf[j][dt].z) | nan_bytes(vf[j][dt].w);
                 if (__any(any != 0)) {
-                    // a rare path: opaque() keeps its values from being computed ahead, or
-                    // kept, for all tiles, which cost the loop 80 registers
+                    // a rare path, kept small: the codes are read again, eight tokens
+                    // of 16 dims at a time
+#pragma unroll 1
+                    for (int k = 0; k < DW * 4; ++k) {
+                        const int dt = k >> 2, at = 64 * (k >> 1 & 1) + 16 * g, e8 = 8 * (k & 1);
+                        const int page = k & 2 ? id.v[1] : id.v[0];
+                        const bool ok = valid(page);
+                        const uint2 c = *reinterpret_cast<const uint2 *>(
+                            a.c.v + ((int64_t)(ok ? page : 0) * a.c.heads + h) * page_bytes +
+                            (((wave * DW + dt) * 16 + r) << a.c.lp) + (at & pmask) + e8);
+                        const bf16x8 ones = bf16x8_of(nan_ones(c.x), nan_ones(c.y), 1.0f);
 #pragma unroll
-                    for (int dt = 0; dt < DW; ++dt)
+                        for (int rt = 0; rt < RT; ++rt) {
+                            union {
+                                uint32_t w[4];
+                                bf16x8 v;
+                            } u;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint32_t &lo = e ? vf[j][dt].z : vf[j][dt].x, &hi = e ? vf[j][dt].w : vf[j][dt].y;
-                                lo = opaque(lo);
-                                hi = opaque(hi);
-                                const bf16x8 ones = bf16x8_of(nan_ones(lo), nan_ones(hi), 1.0f);
-                                lo = opaque(without_nan(lo));
-                                hi = opaque(without_nan(hi));
-#pragma unroll
-                                for (int rt = 0; rt < RT; ++rt) {
-                                    const int t = (int)opaque(t0 + 64 * j + 16 * g + 8 * e);
-                                    union {
-                                        uint32_t w[4];
-                                        bf16x8 v;
-                                    } u;
-#pragma unroll
-                                    for (int i = 0; i < 8; i += 2)
-                                        u.w[i / 2] = (v_ok[j] && sees(t + i, pos[rt]) ? 0x3F80u : 0u) |
-                                                     (v_ok[j] && sees(t + i + 1, pos[rt]) ? 0x3F800000u : 0u);
-                                    const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, u.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) poison[rt] |= n[i] > 0.0f ? 1u << (4 * dt + i) : 0u;
-                                    poison[rt] = opaque(poison[rt]);
-                                }
+                            for (int i = 0; i < 8; i += 2) {
+                                const int t = t0 + at + e8 + i;
+                                u.w[i / 2] = (ok & sees(t, pos[rt]) ? 0x3F80u : 0u) | (ok & sees(t + 1, pos[rt]) ? 0x3F800000u : 0u);
                             }
+                            const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, u.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) poison[rt] |= n[i] > 0.0f ? 1u << (4 * dt + i) : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int dt = 0; dt < DW; ++dt)
+                            vf[j][dt] = make_uint4(without_nan(vf[j][dt].x), without_nan(vf[j][dt].y), without_nan(vf[j][dt].z),
+                                                   without_nan(vf[j][dt].w));
                 }
             }
 #pragma unroll

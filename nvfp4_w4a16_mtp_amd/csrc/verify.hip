@@ -39,7 +39,7 @@ struct VPart {
     double sum;             // of exp((l - max) / T) over the chunk (fp64 sums of outright
                             // drafts: without the draft's own term)
     float max;
-    int idx;                // of the first maximum (-1: nothing above -inf)
+    int idx;                // of the first maximum (-1: nothing above -inf); greedy sequences alone
 };
 
 // 2^(d c) for d c in [-1022, 0]: d c = n + r with n an integer (the sum with 1.5 *
@@ -165,8 +165,8 @@ constexpr int kVThreads = 256;
 // groups of 16 bytes.  WAVES = 1: no barriers, the loads of a workgroup's four
 // chunks overlap with each other's sums (many rows).  WAVES = 4: a quarter of the
 // terms per lane (few rows, where one chunk's time counts).  EXACT: fp64 terms.
-// Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5 (30 binary digits
-// of an argument, 32 fp32 additions), which decides every draft but those next to
+// Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5 (2^-23 of arguments
+// up to 40 and of the maximum's, 32 fp32 additions), which decides every draft but those next to
 // the border (see decide), and the drawn row is summed again.
 template <bool BF16, int WAVES, bool EXACT>
 __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds, bool vec) {
@@ -195,10 +195,10 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             mx = fmaxf(mx, x[g][j]);
-            nan |= x[g][j] != x[g][j];
+            if (EXACT) nan |= x[g][j] != x[g][j];     // (an fp32 sum becomes NaN by itself)
         }
     const float own = mx;
-    nan = __any(nan);
+    nan = EXACT && __any(nan);
     for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m, 64));
     __shared__ float smax[4];
     __shared__ bool snan[4];
@@ -216,14 +216,16 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
             nan |= snan[v];
         }
     }
-    // the first index that has the maximum
+    // greedy: the first index that has the maximum
     int mi = 0x7FFFFFFF;
-    if (own == mx && mx > -INFINITY)
+    if (!(it > 0.0)) {
+        if (own == mx && mx > -INFINITY)
 #pragma unroll
-        for (int g = G - 1; g >= 0; --g)
+            for (int g = G - 1; g >= 0; --g)
 #pragma unroll
-            for (int j = E - 1; j >= 0; --j) mi = x[g][j] == mx ? c0 + (g * T + tid) * E + j : mi;
-    for (int m = 1; m < 64; m <<= 1) mi = min(mi, __shfl_xor(mi, m, 64));
+                for (int j = E - 1; j >= 0; --j) mi = x[g][j] == mx ? c0 + (g * T + tid) * E + j : mi;
+        for (int m = 1; m < 64; m <<= 1) mi = min(mi, __shfl_xor(mi, m, 64));
+    }
     double sum = 0.0;
     if (it > 0.0) {
         if (id >= c0 && id < c1) {
@@ -241,12 +243,12 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum += term_above(x[g][j], ref, low, it);
         } else {
-            const float c = (float)it;
+            const float c = (float)it, shift = -ref * c;
             float part = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f((x[g][j] - ref) * c);
+                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][j], c, shift));
             sum = part;
         }
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
         VPart p;
         p.sum = nan ? NAN : it > 0.0 && mx > -INFINITY ? sum : 0.0;
         p.max = mx;
-        p.idx = mx > -INFINITY ? mi : -1;
+        p.idx = mx > -INFINITY && !(it > 0.0) ? mi : -1;
         a.part[((int64_t)(b * a.max_rows + i) * kinds + kind) * a.chunks + chunk] = p;
     }
 }
@@ -322,6 +324,29 @@ __device__ __forceinline__ double row_sum(const VerifyArgs &a, int64_t row, floa
     return sum;
 }
 
+// The first index of a row's maximum by the whole workgroup (0: nothing above -inf).
+template <bool BF16>
+__device__ __forceinline__ int row_first_max(const VerifyArgs &a, int64_t row) {
+    __shared__ float pmax[kDecideThreads / 64];
+    __shared__ int pidx[kDecideThreads / 64];
+    float mx = -INFINITY;
+    int mi = -1;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < a.vocab; e += kDecideThreads) take_max(mx, mi, logit<BF16>(a.logits, row * a.stride + e), e);
+    if (mx == -INFINITY) mi = -1;
+    for (int m = 1; m < 64; m <<= 1) take_max(mx, mi, __shfl_xor(mx, m, 64), __shfl_xor(mi, m, 64));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        pmax[threadIdx.x >> 6] = mx;
+        pidx[threadIdx.x >> 6] = mi;
+    }
+    __syncthreads();
+    mx = -INFINITY;
+    mi = -1;
+    for (int i = 0; i < kDecideThreads / 64; ++i) take_max(mx, mi, pmax[i], pidx[i]);
+    return mx > -INFINITY ? mi : 0;
+}
+
 // One workgroup of kDecideThreads: where sequence b stops and how its token is
 // drawn.  The test u q(d) < p(d) is u wq sum_p < wd sum_q with the drafts' terms wd,
 // wq; with fp32 sums a test whose sides agree to 2^-16 is made again with the row's
@@ -331,7 +356,7 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
     __shared__ VRow sp[kMaxRows], sq[kMaxRows];
     __shared__ double swd[kMaxRows];
     __shared__ float sua[kMaxRows];
-    __shared__ int sstop[kMaxRows], sid[kMaxRows];    // 2: too close to tell
+    __shared__ int sstop[kMaxRows], sid[kMaxRows];    // 2: too close to tell, 3: no softmax
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int i = wave; i < q.n; i += kDecideThreads / 64) {
         const VPart *p = a.part + ((int64_t)(b * a.max_rows + i) * kinds) * a.chunks;
@@ -352,8 +377,10 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
                 if (kinds == 1 && a.exact) rp.sum += wd;
             }
             if (kinds == 2) rq = join_chunks(p + a.chunks, a.chunks, it, lane);
-            if (!(it > 0.0) || !rp.finite()) {
+            if (!(it > 0.0)) {
                 stop = id != max(rp.idx, 0);
+            } else if (!rp.finite()) {
+                stop = 3;
             } else if (in) {
                 double lhs = (double)ua * rp.sum, rhs = wd;
                 if (kinds == 2 && rq.finite()) {
@@ -374,9 +401,14 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
         }
     }
     __syncthreads();
-    int at = 0;
+    int at = 0, best = 0;
     for (;; ++at) {                                   // the last row always stops
         int stop = sstop[at];
+        best = max(sp[at].idx, 0);
+        if (stop == 3 || (at == q.n - 1 && it > 0.0 && !sp[at].finite())) {
+            best = row_first_max<BF16>(a, q.r0 + at);
+            stop = at == q.n - 1 || sid[at] != best;
+        }
         if (stop == 2) stop = !((double)sua[at] * row_sum<BF16>(a, q.r0 + at, sp[at].max, it) < swd[at]);
         if (stop) break;
     }
@@ -384,7 +416,7 @@ __device__ __forceinline__ void decide(const VerifyArgs &a, int b, const VSeq &q
     const VRow rp = sp[at], rq = sq[at];
     d.row = at;
     d.draft = sid[at];
-    d.best = max(rp.idx, 0);
+    d.best = best;
     d.pmax = rp.max;
     d.psum = rp.sum;
     d.qmax = rq.max;
@@ -499,7 +531,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
         decide<BF16>(a, b, q, it, kinds, d);
     __shared__ int schunk, smode, shit[kDecideThreads / 64], slast[kDecideThreads / 64];
     __shared__ double starget, wsum[kDecideThreads / 64];
-    int token = d.best;
+    int token = d.mode == kWithout ? d.draft : d.best;   // (kWithout: should nothing else have weight)
     if (d.mode != kGreedy) {
         const VPart *part = a.part + ((int64_t)(b * a.max_rows + d.row) * kinds) * a.chunks;
         const double *rest = a.rest + (int64_t)b * a.chunks;
@@ -600,7 +632,7 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_pick(VerifyArgs a, in
                 found = found < 0 ? shit[i] : found;
                 fall = slast[i] >= 0 ? slast[i] : fall;
             }
-            token = found >= 0 ? found : (fall >= 0 ? fall : d.best);
+            token = found >= 0 ? found : (fall >= 0 ? fall : token);
         }
     }
     for (int i = tid; i < q.n; i += kDecideThreads)
