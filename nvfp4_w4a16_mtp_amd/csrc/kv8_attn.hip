@@ -217,6 +217,11 @@ struct Shares {
     }
 };
 
+// Workgroups a CU holds at once (a wavefront of each on every SIMD): enough loads in
+// flight, and no more shares than that.  One row each of 32 sequences, D = 256: 100 us
+// with 2, 106 with 3; windowed decode, D = 128: 101 with 2, 92 with 3, 96 with 4.
+constexpr int groups_per_cu(int d, int rt) { return rt == 4 || d >= 192 ? 2 : d == 128 ? 3 : 4; }
+
 // One workgroup: a share of the steps.  EVEN: the steps of all (sequence, kv head)
 // pairs in order are cut into equal shares, so that every workgroup reads the same
 // number of keys however ragged the batch is (one row tile a sequence).  Else: 16 *
@@ -226,7 +231,7 @@ struct Shares {
 // workgroup to arrive instead, through device-scope accesses: 114 against 111 us for
 // one row each of 32 sequences, 102 against 80 us with 3 to 6 rows of 16.)
 template <int D, int RT, bool EVEN>
-__global__ __launch_bounds__(256, (RT == 4 ? 2 : D * RT <= 256 ? 4 - (D * RT > 128) : 2)) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)) void k_attn(AttnArgs a) {
     constexpr int C = D / 64, DW = D / 64;            // 64-element chunks; 16-dim tiles of a wavefront
     __shared__ Shared<D, RT> sh;
     __shared__ int before[EVEN ? kMaxShared + 1 : 1], wave_sum[4];
@@ -682,7 +687,8 @@ static AttnPlan attn_plan(const nvfp4_kv8_cache *c, const nvfp4_kv8_seqs *s, int
     const int64_t steps = (len + kStep - 1) / kStep;
     // even shares keep the step count in 32 bits
     p.even = p.row_tiles == 1 && s->batch <= kMaxShared && units * ((cap + kStep - 1) / kStep + 1 + kSetup) < (1LL << 30);
-    const int64_t slots = (int64_t)num_cus() * blocks_per_cu(attn_kernel(c->head_dim, p.rt, p.even), 256, 0);
+    const int fit = blocks_per_cu(attn_kernel(c->head_dim, p.rt, p.even), 256, 0), want_cu = groups_per_cu(c->head_dim, p.rt);
+    const int64_t slots = (int64_t)num_cus() * (fit < want_cu ? fit : want_cu);
     p.splits = 1;
     bool pieces;
     if (p.even) {
