@@ -115,6 +115,8 @@ struct RopeTask {
     int heads;
 };
 
+constexpr int kHeads = 2;   // heads whose loads are in flight together
+
 __device__ __forceinline__ void rope_unit(const RopeTask &t, const Rope &rp, int64_t row, int u, int h0, int h1,
                                           double pos) {
     const int turns = rp.rot >> 4;
@@ -130,12 +132,23 @@ __device__ __forceinline__ void rope_unit(const RopeTask &t, const Rope &rp, int
     Turn8 w;
     w.load(rp, pos, u * 8);
     const int d0 = rp.inter ? u * 16 : u * 8, d1 = rp.inter ? d0 + 8 : d0 + (rp.rot >> 1);
-    for (int h = h0; h < h1; ++h) {
-        uint4 x = *reinterpret_cast<const uint4 *>(src + h * t.in.head + d0);
-        uint4 y = *reinterpret_cast<const uint4 *>(src + h * t.in.head + d1);
-        w.apply(x, y, rp.inter);
-        *reinterpret_cast<uint4 *>(dst + h * t.out.head + d0) = x;
-        *reinterpret_cast<uint4 *>(dst + h * t.out.head + d1) = y;
+    // the loads of kHeads heads at a time (past the last one, the last again)
+    for (int h = h0; h < h1; h += kHeads) {
+        uint4 x[kHeads], y[kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+            const uint16_t *at = src + (int64_t)min(h + k, h1 - 1) * t.in.head;
+            x[k] = *reinterpret_cast<const uint4 *>(at + d0);
+            y[k] = *reinterpret_cast<const uint4 *>(at + d1);
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+            if (h + k >= h1) break;
+            w.apply(x[k], y[k], rp.inter);
+            uint16_t *at = dst + (int64_t)(h + k) * t.out.head;
+            *reinterpret_cast<uint4 *>(at + d0) = x[k];
+            *reinterpret_cast<uint4 *>(at + d1) = y[k];
+        }
     }
 }
 
@@ -491,13 +504,15 @@ static int rope_units(const RopeTask &t, int dim, int rot) {
     return rot / 16 + (t.in.data == t.out.data ? 0 : (dim - rot) / 8);
 }
 
-// Heads a thread turns with one set of angles: as many as leave the device
-// about four workgroups per CU (the angles are most of the arithmetic).
+// Heads a thread turns with one set of angles: as many as leave the device about
+// four workgroups per CU, four at most (the angles are most of the arithmetic, but
+// fewer heads keep more loads in flight: 6001 rows of 32 + 8 heads of 128, 33.3 us
+// with seven heads a thread, 29.9 with four).
 static int heads_per_thread(int64_t threads_per_head, int heads) {
     const int64_t want = (int64_t)num_cus() * 4 * 256;
     int64_t per = threads_per_head * heads / want;
     per = per < 1 ? 1 : per;
-    return (int)(per < 8 ? per : 8);
+    return (int)(per < 4 ? per : 4);
 }
 
 }  // namespace nvfp4

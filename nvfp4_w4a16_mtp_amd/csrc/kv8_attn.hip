@@ -220,7 +220,7 @@ struct Shares {
 // Workgroups a CU holds at once (a wavefront of each on every SIMD): enough loads in
 // flight, and no more shares than that.  One row each of 32 sequences, D = 256: 100 us
 // with 2, 106 with 3; windowed decode, D = 128: 101 with 2, 92 with 3, 96 with 4.
-constexpr int groups_per_cu(int d, int rt) { return rt == 4 || d >= 192 ? 2 : d == 128 ? 3 : 4; }
+constexpr int groups_per_cu(int d, int rt) { return rt >= 3 || d >= 192 ? 2 : d == 128 ? 3 : 4; }
 
 // One workgroup: a share of the steps.  EVEN: the steps of all (sequence, kv head)
 // pairs in order are cut into equal shares, so that every workgroup reads the same
@@ -666,9 +666,9 @@ template <int D>
 static const void *attn_kernel(int rt, bool even) {
     if (even)
         return rt == 1 ? reinterpret_cast<const void *>(k_attn<D, 1, true>)
-                       : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, true>) : reinterpret_cast<const void *>(k_attn<D, 4, true>);
+                       : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, true>) : rt == 3 ? reinterpret_cast<const void *>(k_attn<D, 3, true>) : reinterpret_cast<const void *>(k_attn<D, 4, true>);
     return rt == 1 ? reinterpret_cast<const void *>(k_attn<D, 1, false>)
-                   : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, false>) : reinterpret_cast<const void *>(k_attn<D, 4, false>);
+                   : rt == 2 ? reinterpret_cast<const void *>(k_attn<D, 2, false>) : rt == 3 ? reinterpret_cast<const void *>(k_attn<D, 3, false>) : reinterpret_cast<const void *>(k_attn<D, 4, false>);
 }
 static const void *attn_kernel(int dim, int rt, bool even) {
     return dim == 64 ? attn_kernel<64>(rt, even)
@@ -679,7 +679,7 @@ static AttnPlan attn_plan(const nvfp4_kv8_cache *c, const nvfp4_kv8_seqs *s, int
     AttnPlan p{};
     const int max_rows = s->max_rows < s->rows ? s->max_rows : s->rows;
     const int64_t rows = (int64_t)max_rows * (q_heads / c->kv_heads);
-    p.rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.rt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4;
     p.row_tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
     const int64_t units = (int64_t)s->batch * c->kv_heads * p.row_tiles;
     const int64_t cap = (int64_t)s->max_pages * c->page_tokens;
@@ -718,10 +718,12 @@ static void launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
     if (p.even) {
         if (p.rt == 1) launch_attn<D, 1, true>(p, a, s);
         else if (p.rt == 2) launch_attn<D, 2, true>(p, a, s);
+        else if (p.rt == 3) launch_attn<D, 3, true>(p, a, s);
         else launch_attn<D, 4, true>(p, a, s);
     } else {
         if (p.rt == 1) launch_attn<D, 1, false>(p, a, s);
         else if (p.rt == 2) launch_attn<D, 2, false>(p, a, s);
+        else if (p.rt == 3) launch_attn<D, 3, false>(p, a, s);
         else launch_attn<D, 4, false>(p, a, s);
     }
 }
