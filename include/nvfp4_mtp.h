@@ -610,7 +610,8 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  *               changes nothing).
  *   out         bf16, row r head h at out + r * out_row_stride + h * head_dim
  *               (the o projection's activation row), 16-byte aligned,
- *               out_row_stride a multiple of 8, >= q_heads * head_dim.
+ *               out_row_stride a multiple of 8, >= q_heads * head_dim;
+ *               must not overlap q.
  *               A row that sees no token becomes zero; rows outside every
  *               sequence are left as they were.
  *   workspace   kv8_attention_workspace_bytes(cache, seqs, q_heads) bytes,
@@ -667,8 +668,8 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
  *   workspace    verify_drafts_workspace_bytes(batch, max_rows, vocab,
  *                draft_logits != NULL) bytes, 16-byte aligned; nothing to
  *                initialise; one call at a time per workspace.
- * int32 and fp32 arrays 4-byte aligned.  Two launches (three with
- * draft_logits).
+ * int32 and fp32 arrays 4-byte aligned.  Two launches (few rows of outright
+ * drafts) or four.
  */
 size_t verify_drafts_workspace_bytes(int32_t batch, int32_t max_rows, int32_t vocab, int32_t with_draft_logits);
 int verify_drafts(const void *logits, int32_t logits_dtype, int64_t row_stride, int32_t vocab, const void *draft_logits,

@@ -589,7 +589,8 @@ static int append(const char *who, const nvfp4_kv8_cache *cache, const nvfp4_kv8
     a.kv_blocks = (int)kv_blocks;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (rope) {
-        const size_t lds = (size_t)P * a.rp.rot * 2;  // at most 64 KiB
+        const size_t lds = (size_t)P * a.rp.rot * 2;  // at most 64 KiB, and 64 bytes of the kernel's own
+        if (int rc = allow_lds(reinterpret_cast<const void *>(k_append<true>), lds + 64, who)) return rc;
         hipLaunchKernelGGL(k_append<true>, dim3((unsigned)blocks), dim3(threads), lds, s, a);
     } else {
         hipLaunchKernelGGL(k_append<false>, dim3((unsigned)blocks), dim3(threads), 0, s, a);

@@ -763,6 +763,9 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
     if (out_row_stride % 8 || out_row_stride < (int64_t)q->heads * q->dim)
         return fail(NVFP4_ERR_SHAPE, "%s: out_row_stride=%lld must be a multiple of 8 and >= q_heads * head_dim", who,
                     (long long)out_row_stride);
+    if ((int64_t)seqs->max_rows * (q->heads / cache->kv_heads) >= (1LL << 30))
+        return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_rows=%d rows of %d query heads a kv head are too many", who, seqs->max_rows,
+                    q->heads / cache->kv_heads);
     const AttnPlan p = attn_plan(cache, seqs, q->heads);
     if (p.blocks > 2147483647LL || p.join_blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     if (!workspace || ws_bytes < p.ws)

@@ -62,11 +62,10 @@ __device__ __forceinline__ double exp2_neg(double d, double c) {
     const uint32_t hi = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)u);
 }
-// The lowest logit whose term is taken as it is: terms far below the maximum (and
-// NaN) become 2^-1000, nothing beside the maximum's 1.
-__device__ __forceinline__ float lowest(float max, double c) { return (float)fmax((double)max - 1000.0 / c, -3.0e38); }
-__device__ __forceinline__ double term_above(float l, float max, float low, double c) {
-    return exp2_neg((double)fmaxf(l, low) - (double)max, c);
+// The same without exact zeros: terms far below the maximum, of -inf and of NaN
+// become 2^-1000, nothing beside the maximum's 1.  low = -1000 / c.
+__device__ __forceinline__ double term_above(float l, float max, double low, double c) {
+    return exp2_neg(fmax((double)l - (double)max, low), c);
 }
 // exp((l - max) / T), c = log2(e) / T: 0 far below the maximum (and for l =
 // -inf), NaN for NaN.
@@ -165,8 +164,8 @@ constexpr int kVThreads = 256;
 // groups of 16 bytes.  WAVES = 1: no barriers, the loads of a workgroup's four
 // chunks overlap with each other's sums (many rows).  WAVES = 4: a quarter of the
 // terms per lane (few rows, where one chunk's time counts).  EXACT: fp64 terms.
-// Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5 (2^-23 of arguments
-// up to 40 and of the maximum's, 32 fp32 additions), which decides every draft but those next to
+// Else fp32 ones (v_exp_f32): the whole is off by less than 1e-5 (2^-22 of arguments
+// up to 40, 32 fp32 additions), which decides every draft but those next to
 // the border (see decide), and the drawn row is summed again.
 template <bool BF16, int WAVES, bool EXACT>
 __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int kinds, bool vec) {
@@ -237,18 +236,18 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
         if (EXACT) {
-            const float low = lowest(ref, it);        // (a NaN is noted)
+            const double low = -1000.0 / it;          // (a NaN is noted)
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum += term_above(x[g][j], ref, low, it);
         } else {
-            const float c = (float)it, shift = -ref * c;
+            const float c = (float)fmin(it, 3.0e38);
             float part = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][j], c, shift));
+                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f((x[g][j] - ref) * c);
             sum = part;
         }
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
@@ -267,7 +266,8 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
     }
     if (tid == 0) {
         VPart p;
-        p.sum = nan ? NAN : it > 0.0 && mx > -INFINITY ? sum : 0.0;
+        // (nothing but terms far below, the excluded draft the only one: no weight)
+        p.sum = nan || sum != sum ? NAN : mx > -INFINITY && sum > 0x1p-900 ? sum : 0.0;
         p.max = mx;
         p.idx = mx > -INFINITY && !(it > 0.0) ? mi : -1;
         a.part[((int64_t)(b * a.max_rows + i) * kinds + kind) * a.chunks + chunk] = p;
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool ve
     const double it = inv_temp(a, b);
     const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab);
     const int64_t row = q.r0 + d.row;
-    const float plow = lowest(d.pmax, it), qlow = d.mode == kRest ? lowest(d.qmax, it) : 0.0f;
+    const double low = -1000.0 / it;
     const double ip = 1.0 / d.psum, iq = 1.0 / d.qsum;
     double sum = 0.0;
 #pragma unroll 2
@@ -489,13 +489,13 @@ __global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool ve
             load_logits<BF16, 8>(a.draft, row * a.dstride, e0, c1, vec, y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double r = term_above(x[i], d.pmax, plow, it) * ip - term_above(y[i], d.qmax, qlow, it) * iq;
+                const double r = term_above(x[i], d.pmax, low, it) * ip - term_above(y[i], d.qmax, low, it) * iq;
                 sum += r > 0.0 ? r : 0.0;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sum += term_above(d.mode == kWithout && e0 + i == d.draft ? -INFINITY : x[i], d.pmax, plow, it);
+                sum += term_above(d.mode == kWithout && e0 + i == d.draft ? -INFINITY : x[i], d.pmax, low, it);
         }
     }
     for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);

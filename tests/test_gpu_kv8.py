@@ -214,7 +214,7 @@ def test_append_bounds():
 
 
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("dim,rot,P", [(64, 64, 16), (256, 64, 16), (128, 96, 64), (192, 192, 128)])
+@pytest.mark.parametrize("dim,rot,P", [(64, 64, 16), (256, 64, 16), (128, 96, 64), (192, 192, 128), (256, 256, 128)])
 def test_fused_equals_the_two_calls(inter, dim, rot, P):
     nv = nvm()
     rng = np.random.default_rng(dim + rot)
@@ -239,6 +239,20 @@ def test_fused_equals_the_two_calls(inter, dim, rot, P):
     third = device_cache(host)
     assert nv.rope_kv8_append(third, s, None, k, v, freq, interleaved=inter, mscale=1.1) is None
     assert torch.equal(third.k_codes, one.k_codes)
+
+
+def test_fused_leaves_rows_outside_the_sequences():
+    nv = nvm()
+    rng = np.random.default_rng(14)
+    host = ref.Cache(3, 2, 16, 64, rng)
+    dev = device_cache(host)
+    q, k, v = (bf(rng.normal(0, 1, (6, h, 64))) for h in (4, 2, 2))
+    freq = torch.from_numpy(1e4 ** (-np.arange(0, 64, 2) / 64)).cuda()
+    q_out = torch.full_like(q, 3.0)
+    nv.rope_kv8_append(dev, seqs([1, 3, 4], [2, 20], np.array([[0, 1], [1, 2]]), 2), q, k, v, freq, q_out=q_out)
+    assert bool((q_out[0] == 3).all()) and bool((q_out[4:] == 3).all()) and not bool((q_out[1:4] == 3).all())
+    want, _ = nv.rope_qk(q[1:4], None, i32([0, 1, 19]), freq)
+    assert torch.equal(q_out[1:4], want)
 
 
 # -------------------------------------------------------------- attention

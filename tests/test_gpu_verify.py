@@ -102,6 +102,18 @@ def test_verify_border_random_numbers(sampled):
                 check(logits, cu, ids, np.full(24, ua), np.full(8, us), draft=draft if sampled else None)
 
 
+@pytest.mark.parametrize("batch", [1, 80])
+def test_verify_first_draw_behind_masked_chunks(batch):
+    """u_sample = 0 with nothing but the fallen draft in the first chunks."""
+    vocab, live = 20000, [14000, 14001, 19999]
+    logits = np.full((2 * batch, vocab), -np.inf)
+    logits[:, live] = 1.0
+    logits[::2, 17] = 1.5
+    cu, ids = np.arange(0, 2 * batch + 1, 2), np.full(2 * batch, 17)
+    out = check(logits, cu, ids, np.full(2 * batch, 0.999), np.zeros(batch))
+    assert np.all(out[0] == 0) and np.all(out[2] == 14000)
+
+
 @pytest.mark.parametrize("sampled", [False, True])
 def test_verify_rows_without_a_softmax(sampled):
     """NaN, +inf, nothing above -inf: the greedy scan; ids out of range fall."""
@@ -125,6 +137,24 @@ def test_verify_rows_without_a_softmax(sampled):
     logits[14, ids[14]] = -np.inf
     out = check(logits, cu, ids, ua, us, draft=draft if sampled else None)
     assert out[0][0] == 1 and out[0][1] == 1 and out[0][2] == 1 and out[0][3] == 0 and out[0][5] == 0 and out[0][6] == 0
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+@pytest.mark.parametrize("vocab,batch", [(3000, 3), (20011, 60)])
+def test_verify_far_from_zero(vocab, batch, sampled):
+    """Logits with a large common offset, tokens masked with the type's lowest
+    value, temperatures at the ends of fp32."""
+    rng = np.random.default_rng(vocab)
+    cu, logits, draft, ids, ua, us = make(rng, [3] * batch, vocab, peak=3.0)
+    logits, draft = np.round(logits * 64) / 64 + 30000.0, np.round(draft * 64) / 64 + 30000.0
+    lowest = float(np.finfo(np.float32).min)
+    for r in range(0, len(ids), 4):
+        mask = rng.random(vocab) < 0.9
+        mask[ids[r]] = False
+        logits[r, mask], draft[r, mask] = lowest, lowest
+    temp = rng.choice([0.3, 1.0, 1.7], batch)
+    temp[:3] = [1e-38, 3e38, 0.02]
+    check(logits, cu, ids, ua * 0.3, us, temp=temp, draft=draft if sampled else None)
 
 
 def test_verify_temperatures():
