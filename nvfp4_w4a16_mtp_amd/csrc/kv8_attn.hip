@@ -28,6 +28,8 @@
 //
 // P is rounded to bf16 (2^-8 relative at most) for the matrix cores, and the row's
 // sum is of the rounded values: a row with one large weight comes out exact.
+#include <type_traits>
+
 #include "kv8.hpp"
 
 namespace nvfp4 {
@@ -625,28 +627,37 @@ __global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int grid) {
     const int rows = min(sq.n, a.s.max_rows) * (int)a.group.d;
     const int row = ((a.row_tiles - 1 - tile % a.row_tiles) * RT + rt) * 16 + r;
     if (row >= rows) return;
-    constexpr int N = 8;                              // pieces whose loads are in flight together
     float mx = -INFINITY, sum = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < pieces.count; k0 += N) {
-        float2 ml[N];
-        f32x4 v[N];
+    // n pieces at a time, their loads in flight together
+    auto add = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        for (int k0 = 0; k0 < pieces.count; k0 += N) {
+            float2 ml[N];
+            f32x4 v[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float *p = a.part + ((int64_t)pieces.at(min(k0 + k, pieces.count - 1)) * RT + rt) * part_floats<D>();
-            ml[k] = *reinterpret_cast<const float2 *>(p + 16 * D + 2 * r);
-            v[k] = *reinterpret_cast<const f32x4 *>(p + dt * 256 + lane * 4);
-        }
+            for (int k = 0; k < N; ++k) {
+                const float *p = a.part + ((int64_t)pieces.at(min(k0 + k, pieces.count - 1)) * RT + rt) * part_floats<D>();
+                ml[k] = *reinterpret_cast<const float2 *>(p + 16 * D + 2 * r);
+                v[k] = *reinterpret_cast<const f32x4 *>(p + dt * 256 + lane * 4);
+            }
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if (k0 + k >= pieces.count) continue;
-            const float mn = fmaxf(mx, ml[k].x), ref = mn == -INFINITY ? 0.0f : mn;
-            const float fa = __builtin_amdgcn_exp2f(mx - ref), fb = __builtin_amdgcn_exp2f(ml[k].x - ref);
-            sum = sum * fa + ml[k].y * fb;
-            o = o * fa + v[k] * fb;
-            mx = mn;
+            for (int k = 0; k < N; ++k) {
+                if (k0 + k >= pieces.count) continue;
+                const float mn = fmaxf(mx, ml[k].x), ref = mn == -INFINITY ? 0.0f : mn;
+                const float fa = __builtin_amdgcn_exp2f(mx - ref), fb = __builtin_amdgcn_exp2f(ml[k].x - ref);
+                sum = sum * fa + ml[k].y * fb;
+                o = o * fa + v[k] * fb;
+                mx = mn;
+            }
         }
-    }
+    };
+    // (one token over 1500 keys, 12 pieces: 12.6 us eight at a time, 11.9 sixteen; a
+    // windowed batch, two or three pieces: 91.7 and 93.0)
+    if (pieces.count <= 4)
+        add(std::integral_constant<int, 4>{});
+    else
+        add(std::integral_constant<int, 16>{});
     const int i = a.group.div(row), hq = h * (int)a.group.d + row - i * (int)a.group.d;
     store_out(a.out + (int64_t)(sq.r0 + i) * a.out_stride + (int64_t)hq * D + dt * 16 + 4 * (lane >> 4),
               o * (sum == 0.0f ? 0.0f : 1.0f / sum));
