@@ -657,11 +657,13 @@ def moe_layer_w4a16(x: torch.Tensor, router: NVFP4Weight, top_k: int, experts: N
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_BF16 = torch.bfloat16
 
 
 def _run(what: str, fn, index: int, *args):
     """fn(*args, stream) on device `index` and its current stream."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:      # (a tensor on the device: CUDA is initialised)
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -685,7 +687,7 @@ def _same_device(index: int, *tensors):
 def _rows(t: torch.Tensor, name: str) -> _HeadRows:
     """Head rows of a bf16 [rows][heads][dim] tensor (unit stride in dim)."""
     shape = t.shape
-    if t.dtype is not torch.bfloat16 or len(shape) != 3:
+    if t.dtype is not _BF16 or len(shape) != 3:
         raise ValueError(f"{name} must be bf16 [rows][heads][dim]")
     n, heads, dim = shape
     row, head, unit = t.stride()
@@ -812,26 +814,28 @@ def rope_qk(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Ten
     (either may be None; rows and heads may be strided).  Returns (q_out,
     k_out); pass q_out=q to rotate in place."""
     _int32(positions, "positions")
-    rows, index = positions.numel(), positions.get_device()
-    refs, outs = [], []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            refs += [None, None]
-            outs.append(None)
-            continue
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if x.shape[0] != rows or out.shape != x.shape:
-            raise ValueError(f"{name} and {name}_out must have {rows} rows and one shape")
-        _same_device(index, x, out)
-        refs += [ctypes.byref(_rows(x, name)), ctypes.byref(_rows(out, name + "_out"))]
-        outs.append(out)
-    _same_device(index, inv_freq)
-    _run("rope_qk", lib().rope_qk, index, *refs, rows, positions.data_ptr(),
-         ctypes.byref(_rope_desc(inv_freq, interleaved, mscale)))
-    return tuple(outs)
+    rows, index, byref = positions.numel(), positions.get_device(), ctypes.byref
+    dq = dqo = dk = dko = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq, dqo = byref(_rows(q, "q")), byref(_rows(q_out, "q_out"))
+        if q.shape[0] != rows or q_out.shape != q.shape:
+            raise ValueError(f"q and q_out must have {rows} rows and one shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dk, dko = byref(_rows(k, "k")), byref(_rows(k_out, "k_out"))
+        if k.shape[0] != rows or k_out.shape != k.shape:
+            raise ValueError(f"k and k_out must have {rows} rows and one shape")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _same_device(index, q, q_out, k, k_out, inv_freq)
+    _run("rope_qk", lib().rope_qk, index, dq, dqo, dk, dko, rows, positions.data_ptr(),
+         byref(_rope_desc(inv_freq, interleaved, mscale)))
+    return q_out, k_out
 
 
 def kv8_append(cache: KV8Cache, seqs: KV8Seqs, k: torch.Tensor, v: torch.Tensor):
