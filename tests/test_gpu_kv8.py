@@ -389,6 +389,32 @@ def test_attention_strided_rows():
     assert torch.equal(buf[:, 1:9], want) and bool((buf[:, [0, 9]] == 2).all())
 
 
+def test_attention_shared_pages_and_two_streams_at_once():
+    """Sequences that share the pages of a common beginning; two calls on two
+    streams with workspaces of their own."""
+    nv = nvm()
+    rng = np.random.default_rng(27)
+    host = ref.Cache(20, 2, 16, 256, rng)
+    dev = device_cache(host)
+    table = np.array([[4, 9, 9, 7, 1], [4, 9, 9, 3, 2], [4, 9, 9, 3, 2]], np.int32)   # one page twice as well
+    cu, lens = [0, 2, 3, 5], [70, 66, 80]
+    q = normal(rng, (5, 16, 256))
+    want, bound, _ = ref.attention(q, host, table, cu, lens, 1 / 16)
+    s, qd = seqs(cu, lens, table, 2), bf(q)
+    one = nv.kv8_attention(qd, dev, s)
+    assert np.all(np.abs(f64(one) - want) <= bound)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [nv.kv8_attention_workspace(dev, s, 16, 5) for _ in streams]
+    outs = [torch.zeros_like(one) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, ws, out in zip(streams, wss, outs):
+            with torch.cuda.stream(st):
+                nv.kv8_attention(qd, dev, s, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, one) for o in outs)
+
+
 def test_cache_past_two_gigabytes():
     """Pages whose code offsets pass 2^31 and 2^32 bytes."""
     nv = nvm()
