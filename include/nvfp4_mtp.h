@@ -511,9 +511,10 @@ typedef struct nvfp4_rope {
 } nvfp4_rope;
 
 /* A paged 8-bit KV cache (host descriptor, device pointers).  Codes are
- * E4M3FN; scale byte b stands for 2^(b - 127) (255 reads as 254), one per
- * (page, head) and for K and V each; kv8_append writes bytes of 17 or more.  V lies transposed inside
- * its page, so that the attention's matrix operands load straight from it.
+ * E4M3FN; scale byte b stands for 2^(b - 127) (bytes above 246 read as 246, so
+ * that every value is finite in bf16), one per (page, head) and for K and V
+ * each; kv8_append writes 17 to 246.  V lies transposed inside its page, so that
+ * the attention's matrix operands load straight from it.
  * codes 16-byte aligned; page_tokens 16, 32, 64 or 128; head_dim 64, 128, 192
  * or 256; kv_heads >= 1; num_pages >= 1. */
 typedef struct nvfp4_kv8_cache {
@@ -562,7 +563,7 @@ int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_
  *   k, v   [rows][kv_heads][head_dim] head rows.
  * Per page and head, over the tokens of the page that this call writes: amax =
  * max of the finite |x|; e = the smallest exponent >= -110 with amax <= 448 *
- * 2^e.  A page that the call writes from its first token on takes e; a page it
+ * 2^e, 119 at most (values above 448 * 2^119 = 2.98e38 saturate).  A page that the call writes from its first token on takes e; a page it
  * continues takes max(e, its present exponent), and when that grows the page's
  * earlier codes are re-rounded to it.  code = E4M3 nearest to x * 2^-e (ties
  * to even, saturating at 448; infinities saturate, NaN stays NaN).  Powers of
@@ -588,7 +589,7 @@ int rope_kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, co
 
 /*
  * kv8_read -- the cache's values back in bf16 (a code times a power of two:
- * exact for scale bytes of 17 to 246) for the last n_b tokens of each sequence.
+ * exact for scale bytes from 17 on) for the last n_b tokens of each sequence.
  *   k_out, v_out   [rows][kv_heads][head_dim] head rows; one may be NULL.
  *                  Tokens whose page id is out of range and rows at negative
  *                  positions become zero rows; rows outside every sequence

@@ -701,7 +701,8 @@ class KV8Cache:
     """A paged 8-bit KV cache on the device: k_codes [pages, kv_heads,
     page_tokens, head_dim] and v_codes [pages, kv_heads, head_dim,
     page_tokens] uint8 (E4M3), k_scales and v_scales [pages, kv_heads] uint8
-    (byte b stands for 2^(b - 127)).  The tensors keep their storage."""
+    (byte b stands for 2^(b - 127), at most 2^119).  The tensors keep their
+    storage."""
     k_codes: torch.Tensor
     k_scales: torch.Tensor
     v_codes: torch.Tensor

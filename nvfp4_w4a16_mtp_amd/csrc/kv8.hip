@@ -209,11 +209,11 @@ struct AppendArgs {
 
 constexpr int kMinExp = -110;
 
-// Smallest e >= kMinExp with amax <= 448 * 2^e, amax = 1.m * 2^(x - 127) as
-// bf16 bits (448 = 1.75 * 2^8).
+// Smallest e >= kMinExp with amax <= 448 * 2^e, or kMaxExp; amax = 1.m * 2^(x - 127)
+// as bf16 bits (448 = 1.75 * 2^8).
 __device__ __forceinline__ int scale_exp(uint32_t bits) {
     const int e = (int)(bits >> 7) - 135 + ((bits & 0x7Fu) > 0x60u);
-    return max(e, kMinExp);
+    return min(max(e, kMinExp), kMaxExp);
 }
 
 // ROPE: the k rows are rotated (dynamic LDS: page_tokens * rot bf16).

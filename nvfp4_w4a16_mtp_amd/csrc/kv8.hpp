@@ -39,10 +39,12 @@ __device__ __forceinline__ Seq load_seq(const Seqs &s, int b, int lp) {
     return q;
 }
 
-// Scale byte -> exponent of its power of two (255 reads as 254).
-__device__ __forceinline__ int kv8_exp(uint32_t b) { return (int)min(b, 254u) - 127; }
+// Scale byte -> exponent of its power of two, at most 2^119: a larger one would make
+// codes infinite in bf16, and a hidden token's infinity times its weight of 0 is NaN.
+constexpr int kMaxExp = 119;
+__device__ __forceinline__ int kv8_exp(uint32_t b) { return (int)min(b, kMaxExp + 127u) - 127; }
 // ... -> a float with that exponent field, the scale operand of a conversion.
-__device__ __forceinline__ float kv8_scale(uint32_t b) { return __uint_as_float(min(b, 254u) << 23); }
+__device__ __forceinline__ float kv8_scale(uint32_t b) { return __uint_as_float(min(b, kMaxExp + 127u) << 23); }
 
 inline HeadRows view(const nvfp4_head_rows *r) {
     return r ? HeadRows{r->data, r->row_stride, r->head_stride} : HeadRows{nullptr, 0, 0};

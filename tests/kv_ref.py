@@ -5,7 +5,7 @@ import math
 
 import numpy as np
 
-MIN_EXP = -110
+MIN_EXP, MAX_EXP = -110, 119     # of a page's scale; 448 * 2^119 is finite in bf16
 E4M3 = np.array([(-1.0 if b & 128 else 1.0) * ((b & 7) * 2.0 ** -9 if (b >> 3) & 15 == 0 else
                                                (1 + (b & 7) / 8) * 2.0 ** (((b >> 3) & 15) - 7)) for b in range(256)])
 E4M3[[0x7F, 0xFF]] = np.nan
@@ -46,7 +46,7 @@ def scale_exp(amax):
 
 
 def scale_of(byte):
-    return 2.0 ** (min(int(byte), 254) - 127)
+    return 2.0 ** (min(int(byte) - 127, MAX_EXP))
 
 
 class Cache:
@@ -93,10 +93,10 @@ class Cache:
                     for h in range(codes.shape[1]):
                         new = x[rows, h]
                         fin = np.abs(new[np.isfinite(new)])
-                        e = scale_exp(fin.max() if fin.size else 0.0)
+                        e = min(scale_exp(fin.max() if fin.size else 0.0), MAX_EXP)
                         if o0 > 0:
                             s = scale_of(scales[page, h])
-                            e = max(e, int(min(scales[page, h], 254)) - 127)
+                            e = max(e, min(int(scales[page, h]) - 127, MAX_EXP))
                             if s != 2.0 ** e:
                                 old = codes[page, h, :o0]
                                 re = e4m3_encode(E4M3[old] * (s / 2.0 ** e))

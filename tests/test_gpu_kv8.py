@@ -184,6 +184,33 @@ def test_append_special_values():
     same_cache(dev, host)
 
 
+def test_scales_that_bfloat16_cannot_hold():
+    """Values up to the largest bf16: no code is infinite, and hidden tokens of
+    such a page (all larger than the visible ones) reach no row."""
+    nv = nvm()
+    rng = np.random.default_rng(28)
+    host = ref.Cache(4, 2, 16, 64, rng)
+    dev = device_cache(host)
+    table = np.array([[2, 1]], np.int32)
+    k, v = normal(rng, (20, 2, 64)), normal(rng, (20, 2, 64))
+    v[10:] = 3.3895313892515355e38 * rng.choice([-1.0, 1.0], (10, 2, 64))
+    nv.kv8_append(dev, seqs([0, 20], [20], table, 20), bf(k), bf(v))
+    host.append(table, [0, 20], [20], k, v)
+    same_cache(dev, host)
+    assert host.vs.max() == 127 + ref.MAX_EXP
+    _, back = nv.kv8_read(dev, seqs([0, 20], [20], table, 20), rows=20)
+    assert torch.isfinite(back).all()
+    q = normal(rng, (3, 4, 64))
+    for byte in (None, 247, 255):                     # and bytes that only a caller can write
+        if byte is not None:
+            dev.v_scales[2] = byte
+            host.vs[2] = byte
+        for length in (10, 3):                        # tokens 10 .. hold the large ones
+            want, bound, _ = ref.attention(q, host, table, [0, 3], [length], 0.125)
+            got = f64(nv.kv8_attention(bf(q), dev, seqs([0, 3], [length], table, 3), scale=0.125))
+            assert np.all(np.abs(got - want) <= bound), (byte, length)
+
+
 def test_append_bounds():
     """Rows at negative positions, page ids out of range, more rows than
     max_rows, row ranges past the rows: bounded, the rest unharmed."""
