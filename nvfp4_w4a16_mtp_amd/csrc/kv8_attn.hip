@@ -122,7 +122,8 @@ struct Keys {
 __device__ __forceinline__ Keys key_range(int pos_lo, int pos_hi, int window, int sinks) {
     Keys k;
     k.end = max(pos_hi + 1, 0);
-    k.lo_step = window > 0 ? max(pos_lo - window + 1, 0) / kStep : 0;
+    // (rows at negative positions see nothing; their window could pass 32 bits)
+    k.lo_step = window > 0 ? max(max(pos_lo, 0) - window + 1, 0) / kStep : 0;
     const int steps = (k.end + kStep - 1) / kStep;
     k.sink_steps = window > 0 ? min((min(sinks, k.end) + kStep - 1) / kStep, k.lo_step) : 0;
     k.count = k.end > 0 ? k.sink_steps + steps - k.lo_step : 0;
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        pos[rt] = shift + a.group.div(min(row0 + rt * 16 + r, rows - 1));
+        pos[rt] = max(shift + a.group.div(min(row0 + rt * 16 + r, rows - 1)), -1);
         m[rt] = -INFINITY;
         l[rt] = 0.0f;
         poison[rt] = 0u;

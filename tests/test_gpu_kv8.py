@@ -184,6 +184,25 @@ def test_append_special_values():
     same_cache(dev, host)
 
 
+def test_attention_largest_window():
+    """A window of the largest int32 is no window, also for rows that begin
+    before the first token."""
+    nv = nvm()
+    rng = np.random.default_rng(29)
+    host = ref.Cache(12, 2, 16, 64, rng)
+    dev = device_cache(host)
+    table = rng.permutation(12)[:10].reshape(2, 5).astype(np.int32)
+    cu, lens = [0, 12, 92], [3, 70]                   # 9 and 10 rows before the first token
+    q = normal(rng, (92, 4, 64))
+    for rows in (12, 92):                             # one row tile, and several
+        n = cu[:2] if rows == 12 else cu
+        b = len(n) - 1
+        want, bound, _ = ref.attention(q[:rows], host, table[:b], n, lens[:b], 0.125)
+        for window in (2 ** 31 - 1, 2 ** 31 - 6, 0):
+            got = f64(nv.kv8_attention(bf(q[:rows]), dev, seqs(n, lens[:b], table[:b], 80), scale=0.125, window=window))
+            assert np.all(np.abs(got - want) <= bound), (rows, window)
+
+
 def test_scales_that_bfloat16_cannot_hold():
     """Values up to the largest bf16: no code is infinite, and hidden tokens of
     such a page (all larger than the visible ones) reach no row."""
