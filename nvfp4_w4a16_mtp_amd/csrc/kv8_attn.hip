@@ -769,7 +769,8 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
     if (int rc = attn_check(cache, seqs, q->heads, who)) return rc;
     if (q->dim != cache->head_dim) return fail(NVFP4_ERR_SHAPE, "%s: q has dim %d, the cache %d", who, q->dim, cache->head_dim);
     if (window < 0 || sinks < 0) return fail(NVFP4_ERR_ARG, "%s: window=%d or sinks=%d < 0", who, window, sinks);
-    if (!__builtin_isfinite(scale)) return fail(NVFP4_ERR_ARG, "%s: scale is not finite", who);
+    const float scale2 = __builtin_fabsf(scale) * 1.44269504088896340736f;   // for 2^x
+    if (!__builtin_isfinite(scale2)) return fail(NVFP4_ERR_ARG, "%s: scale * log2(e) is not finite", who);
     if (!out) return fail(NVFP4_ERR_ARG, "%s: NULL out", who);
     if (!aligned(out, 16)) return fail(NVFP4_ERR_ALIGN, "%s: out not 16-byte aligned", who);
     if (out_row_stride % 8 || out_row_stride < (int64_t)q->heads * q->dim)
@@ -789,7 +790,7 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
     a.s = view(seqs);
     // at least the smallest normal number: a hidden score of -inf stays -inf, and any
     // finite score times it is 0 to exp2
-    a.scale = __builtin_fmaxf(__builtin_fabsf(scale) * 1.44269504088896340736f, 1.17549435e-38f);
+    a.scale = __builtin_fmaxf(scale2, 1.17549435e-38f);
     a.negate = scale < 0.0f;
     a.window = window;
     a.sinks = sinks;

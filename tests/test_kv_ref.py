@@ -200,6 +200,8 @@ def test_other_refusals():
     assert L.kv8_attention(*ok, 0.1, -1, 0, A, 128, A, 1 << 30, None) == -1
     assert L.kv8_attention(*ok, 0.1, 0, -1, A, 128, A, 1 << 30, None) == -1
     assert L.kv8_attention(*ok, float("nan"), 0, 0, A, 128, A, 1 << 30, None) == -1
+    for scale in (float("inf"), 3e38, -3e38):         # times log2(e) past fp32
+        assert L.kv8_attention(*ok, scale, 0, 0, A, 128, A, 1 << 30, None) == -1
     assert L.kv8_attention(*ok, 0.1, 0, 0, None, 128, A, 1 << 30, None) == -1
     assert L.kv8_attention(*ok, 0.1, 0, 0, A, 120, A, 1 << 30, None) == -2
     assert L.kv8_attention(*ok, 0.1, 0, 0, ctypes.c_void_p(4104), 128, A, 1 << 30, None) == -3
