@@ -488,7 +488,9 @@ int moe_workspace_status(void *workspace, size_t ws_bytes, uint32_t *status, voi
  * data[r * row_stride + h * head_stride + d], strides in elements (a
  * head_stride of 2 * dim reads the q halves of a gated q projection in
  * place).  data 16-byte aligned, both strides multiples of 8, head_stride >=
- * dim, row_stride >= 0. */
+ * dim, row_stride >= 0.  Outputs of two rows or more: also row_stride >= (heads -
+ * 1) * head_stride + dim (token by token), or row_stride >= dim and head_stride >=
+ * (rows - 1) * row_stride + dim (head by head): no two share an element. */
 typedef struct nvfp4_head_rows {
     uint16_t *data;       /* bf16 */
     int64_t row_stride, head_stride;
@@ -552,7 +554,8 @@ typedef struct nvfp4_kv8_seqs {
  *   k, k_out    the same for k; at least one of q and k.
  *   rows        rows of each (0 does nothing).
  *   positions   device int32 [rows], 4-byte aligned, any values.
- * Products and sums in fp64, one rounding to bf16.  dim % 8 == 0.  One launch.
+ * Products and sums in fp64, rounded to fp32 and that to bf16.  dim % 8 == 0.
+ * One launch.
  */
 int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_head_rows *k,
             const nvfp4_head_rows *k_out, int32_t rows, const int32_t *positions, const nvfp4_rope *rope,
@@ -581,7 +584,8 @@ int kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const n
  * sequences, then kv8_append of the rotated k (rounded to bf16, as rope_qk
  * writes it) and v, in one launch: q_out and the cache are bit for bit those
  * of the two calls.  The rotated k is not stored in bf16.  q and q_out may
- * both be NULL.  Rows of q outside every sequence are not written.
+ * both be NULL.  Rows of q outside every sequence are not written; those at
+ * negative positions turn by them.
  */
 int rope_kv8_append(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvfp4_rope *rope,
                     const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_head_rows *k,
@@ -660,7 +664,9 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
  * without a finite sum (NaN, +inf, or nothing above -inf) is taken greedily by
  * the scan of lmhead_gemv_argmax; such a draft row counts as an outright draft.
  *   out_accepted [batch] int32: drafts that stand.
- *   out_tokens   [rows] int32: the standing drafts, the drawn token, then -1.
+ *   out_tokens   [rows] int32: the standing drafts, the drawn token, then -1;
+ *                rows outside every sequence or past max_rows are left as they
+ *                were.
  *   out_next     [batch] int32: the drawn token (-1 for a sequence without
  *                rows).
  *   out_kv_lens  [batch] int32 (with kv_lens; may be kv_lens itself): the

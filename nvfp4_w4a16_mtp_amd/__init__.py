@@ -790,8 +790,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     inv_freq is float64 on `device`."""
     if rot_dim < 16 or rot_dim % 16:
         raise ValueError("rot_dim must be a positive multiple of 16")
-    if not base > 0 or not factor >= 1:
-        raise ValueError("need base > 0 and factor >= 1")
+    if not base > 0 or not factor >= 1 or not high_turns > low_turns:
+        raise ValueError("need base > 0, factor >= 1 and high_turns > low_turns")
     if scaling not in (None, "linear", "base", "by_parts"):
         raise ValueError(f"unknown scaling {scaling!r}")
     if scaling == "base":
@@ -928,7 +928,7 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float 
 
 class Verified(NamedTuple):
     """accepted [batch]: drafts that stand; tokens [rows]: those, the token
-    drawn after them, then -1; next [batch]: the drawn token; kv_lens [batch]:
+    drawn after them, then -1 (rows of no sequence are not written); next [batch]: the drawn token; kv_lens [batch]:
     cache lengths without the fallen drafts' rows (None if not asked for)."""
     accepted: torch.Tensor
     tokens: torch.Tensor

@@ -449,6 +449,15 @@ int validate_head_rows(const nvfp4_head_rows *r, const char *who, const char *wh
     return NVFP4_OK;
 }
 
+// Outputs: no two of `rows` rows' heads share an element.
+static int validate_apart(const nvfp4_head_rows *r, int64_t rows, const char *who, const char *what) {
+    if (rows <= 1 || r->row_stride >= (r->heads - 1) * r->head_stride + r->dim ||
+        (r->row_stride >= r->dim && r->head_stride >= (rows - 1) * r->row_stride + r->dim))
+        return NVFP4_OK;
+    return fail(NVFP4_ERR_SHAPE, "%s: rows of %s overlap (row_stride=%lld, head_stride=%lld)", who, what,
+                (long long)r->row_stride, (long long)r->head_stride);
+}
+
 int validate_kv8_cache(const nvfp4_kv8_cache *c, const char *who) {
     if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
         return fail(NVFP4_ERR_ARG, "%s: NULL cache descriptor or pointer", who);
@@ -486,12 +495,13 @@ static int validate_rope(const nvfp4_rope *r, int dim, const char *who) {
 }
 
 // One of the two rope pairs: both NULL (heads = 0) or both valid and alike.
-static int rope_pair(const nvfp4_head_rows *in, const nvfp4_head_rows *out, const char *who, const char *what,
-                     RopeTask &t) {
+static int rope_pair(const nvfp4_head_rows *in, const nvfp4_head_rows *out, int64_t rows, const char *who,
+                     const char *what, RopeTask &t) {
     t = RopeTask{HeadRows{nullptr, 0, 0}, HeadRows{nullptr, 0, 0}, 0};
     if (!in && !out) return NVFP4_OK;
     if (int rc = validate_head_rows(in, who, what)) return rc;
     if (int rc = validate_head_rows(out, who, what)) return rc;
+    if (int rc = validate_apart(out, rows, who, what)) return rc;
     if (in->heads != out->heads || in->dim != out->dim)
         return fail(NVFP4_ERR_SHAPE, "%s: %s and its output have different heads or dim", who, what);
     if (in->data == out->data && (in->row_stride != out->row_stride || in->head_stride != out->head_stride))
@@ -527,8 +537,8 @@ extern "C" int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, c
     if (rows < 0) return fail(NVFP4_ERR_SHAPE, "%s: rows=%d < 0", who, rows);
     if (rows == 0) return ok();
     RopeTask tq, tk;
-    if (int rc = rope_pair(q, q_out, who, "q", tq)) return rc;
-    if (int rc = rope_pair(k, k_out, who, "k", tk)) return rc;
+    if (int rc = rope_pair(q, q_out, rows, who, "q", tq)) return rc;
+    if (int rc = rope_pair(k, k_out, rows, who, "k", tk)) return rc;
     const int dim = q ? q->dim : k->dim;
     if (q && k && q->dim != k->dim) return fail(NVFP4_ERR_SHAPE, "%s: q and k have different dim", who);
     if (int rc = validate_rope(rope, dim, who)) return rc;
@@ -559,7 +569,7 @@ static int append(const char *who, const nvfp4_kv8_cache *cache, const nvfp4_kv8
             return fail(NVFP4_ERR_SHAPE, "%s: k and v need the cache's kv_heads=%d and head_dim=%d", who, cache->kv_heads,
                         cache->head_dim);
     RopeTask tq;
-    if (int rc = rope_pair(q, q_out, who, "q", tq)) return rc;
+    if (int rc = rope_pair(q, q_out, seqs->rows, who, "q", tq)) return rc;
     if (q && q->dim != cache->head_dim) return fail(NVFP4_ERR_SHAPE, "%s: q has dim %d, the cache %d", who, q->dim, cache->head_dim);
     const int P = cache->page_tokens;
     const int max_rows = seqs->max_rows < seqs->rows ? seqs->max_rows : seqs->rows;
@@ -621,6 +631,7 @@ extern "C" int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs
     for (const nvfp4_head_rows *r : {k_out, v_out}) {
         if (!r) continue;
         if (int rc = validate_head_rows(r, who, r == k_out ? "k_out" : "v_out")) return rc;
+        if (int rc = validate_apart(r, seqs->rows, who, r == k_out ? "k_out" : "v_out")) return rc;
         if (r->heads != cache->kv_heads || r->dim != cache->head_dim)
             return fail(NVFP4_ERR_SHAPE, "%s: outputs need the cache's kv_heads=%d and head_dim=%d", who, cache->kv_heads,
                         cache->head_dim);

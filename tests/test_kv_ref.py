@@ -193,6 +193,14 @@ def test_other_refusals():
     assert L.rope_qk(B(r), B(r), B(_rows(nv, dim=32)), B(_rows(nv, dim=32)), 4, A, B(rp), None) == -2
     assert L.rope_qk(B(r), B(r), None, None, 4, ctypes.c_void_p(4098), B(rp), None) == -3
     assert L.kv8_read(B(c), B(s), None, None, None) == -1
+    # outputs whose rows overlap (4 rows of 2 heads of 64): one row for all, rows
+    # within heads, heads within rows
+    for strides in (dict(row_stride=0), dict(row_stride=64), dict(row_stride=64, head_stride=128), dict(row_stride=120)):
+        o = _rows(nv, **strides)
+        assert L.rope_qk(B(r), B(_rows(nv, data=1 << 20, **strides)), None, None, 4, A, B(rp), None) == -2, strides
+        assert L.rope_qk(None, None, B(o), B(o), 4, A, B(rp), None) == -2, strides
+        assert L.rope_kv8_append(B(c), B(s), B(rp), B(r), B(_rows(nv, data=1 << 20, **strides)), B(r), B(r), None) == -2, strides
+        assert L.kv8_read(B(c), B(s), B(o), None, None) == -2 and L.kv8_read(B(c), B(s), B(r), B(o), None) == -2, strides
     # attention
     q3 = _rows(nv, heads=3, row_stride=192)
     assert L.kv8_attention(B(q3), B(c), B(s), 0.1, 0, 0, A, 192, A, 1 << 30, None) == -2
@@ -225,6 +233,14 @@ def test_other_refusals():
         assert ver(**kw) == rc, kw
     assert ver(batch=0, logits=None, cu=None) == 0
     assert L.verify_drafts_workspace_bytes(2, 65, 100, 0) == 0
+
+
+def test_frequencies_refuse():
+    import nvfp4_w4a16_mtp_amd as nv
+    for kw in (dict(rot_dim=24), dict(rot_dim=0), dict(rot_dim=32, base=0.0), dict(rot_dim=32, factor=0.5),
+               dict(rot_dim=32, scaling="other"), dict(rot_dim=32, scaling="by_parts", low_turns=4.0, high_turns=4.0)):
+        with pytest.raises(ValueError):
+            nv.rope_frequencies(device="cpu", **kw)
 
 
 @built
