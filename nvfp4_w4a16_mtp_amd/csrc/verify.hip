@@ -463,25 +463,29 @@ __global__ __launch_bounds__(kDecideThreads) void k_verify_decide(VerifyArgs a, 
     if (threadIdx.x == 0) a.decided[b] = d;
 }
 
-// Per chunk (a wavefront, four steps of 512 elements) the fp64 sums of what is drawn
-// from: max(p - q, 0), or p, or p without the draft.
-template <bool BF16>
+// Per chunk (WAVES wavefronts, steps of 512 elements) the fp64 sums of what is drawn
+// from: max(p - q, 0), or p, or p without the draft.  Two wavefronts a chunk where one
+// leaves the SIMDs less than four deep (24 sequences' pairs of fp32 rows of 129280: 47.6
+// us the whole call with one, 45.9 with two, 46.1 with four; 64 sequences' bf16 rows of
+// 151936: 53.2, 54.0, 53.8).
+template <bool BF16, int WAVES>
 __global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool vec) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, blocks = (a.chunks + 3) / 4;
-    const int b = blockIdx.x / blocks, chunk = (blockIdx.x - b * blocks) * 4 + wave;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, blocks = (a.chunks * WAVES + 3) / 4;
+    const int b = blockIdx.x / blocks, chunk = ((blockIdx.x - b * blocks) * 4 + wave) / WAVES, part = wave % WAVES;
     const VSeq q = verify_seq(a, b);
-    if (q.n == 0 || chunk >= a.chunks) return;
+    if (q.n == 0) return;
     const Decision d = a.decided[b];
     if (d.mode == kGreedy) return;
     const double it = inv_temp(a, b);
-    const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, a.vocab);
+    // (past the last chunk: the last one again, not stored)
+    const int c0 = min(chunk, a.chunks - 1) * kChunk, c1 = min(c0 + kChunk, a.vocab);
     const int64_t row = q.r0 + d.row;
     const double low = -1000.0 / it;
     const double ip = 1.0 / d.psum, iq = 1.0 / d.qsum;
     double sum = 0.0;
 #pragma unroll 2
-    for (int k = 0; k < 4; ++k) {
-        const int e0 = c0 + k * 512 + lane * 8;
+    for (int k = 0; k < kChunk / 512 / WAVES; ++k) {
+        const int e0 = c0 + (k * WAVES + part) * 512 + lane * 8;
         float x[8];
         load_logits<BF16, 8>(a.logits, row * a.stride, e0, c1, vec, x);
         if (d.mode == kRest) {
@@ -499,8 +503,15 @@ __global__ __launch_bounds__(kVThreads) void k_verify_rest(VerifyArgs a, bool ve
         }
     }
     for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);
+    if (WAVES > 1) {
+        __shared__ double sums[4];
+        if (lane == 0) sums[wave] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) sum += sums[(wave + i) & 3];
+    }
     // a chunk of nothing but terms far below holds no weight
-    if (lane == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum > 0x1p-900 ? sum : 0.0;
+    if (lane == 0 && part == 0 && chunk < a.chunks) a.rest[(int64_t)b * a.chunks + chunk] = sum > 0x1p-900 ? sum : 0.0;
 }
 
 __device__ __forceinline__ double lane_f64(double v, int l) {
@@ -679,7 +690,10 @@ static void launch_verify(const VerifyArgs &a, bool many, bool draft, bool vec, 
         hipLaunchKernelGGL((k_verify_stats<BF16, 1, false>), grid, dim3(kVThreads), 0, s, a, kinds, vec);
     if (a.second) {
         hipLaunchKernelGGL((k_verify_decide<BF16>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds);
-        hipLaunchKernelGGL((k_verify_rest<BF16>), dim3((unsigned)(a.batch * ((a.chunks + 3) / 4))), dim3(kVThreads), 0, s, a, vec);
+        if (a.batch * a.chunks < num_cus() * 16)
+            hipLaunchKernelGGL((k_verify_rest<BF16, 2>), dim3((unsigned)(a.batch * ((a.chunks * 2 + 3) / 4))), dim3(kVThreads), 0, s, a, vec);
+        else
+            hipLaunchKernelGGL((k_verify_rest<BF16, 1>), dim3((unsigned)(a.batch * ((a.chunks + 3) / 4))), dim3(kVThreads), 0, s, a, vec);
     }
     if (a.second)
         hipLaunchKernelGGL((k_verify_pick<BF16, true>), dim3((unsigned)a.batch), dim3(kDecideThreads), 0, s, a, kinds, vec);
