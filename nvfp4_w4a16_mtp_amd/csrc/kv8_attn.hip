@@ -431,18 +431,43 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
             f32x4 s[RT][2];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // Half a chunk at a time: the next half's Q reads and conversions run beside
+            // the products of this one (two prompt chunks 400 us with a chunk's reads and
+            // conversions before its products, 364 so; one row each of 32 sequences 100.7
+            // and 97.0).
+            bf16x8 kc[2][2], qq[2][RT];
+            auto half = [&](int i, bf16x8 (&k)[2]) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const bf16x8 k0[2] = {bf16x8_of(kf[0][c].x, kf[0][c].y, fk[0]), bf16x8_of(kf[0][c].z, kf[0][c].w, fk[0])};
-                const bf16x8 k1[2] = {bf16x8_of(kf[1][c].x, kf[1][c].y, fk[1]), bf16x8_of(kf[1][c].z, kf[1][c].w, fk[1])};
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 w = kf[j][i >> 1];
+                    k[j] = i & 1 ? bf16x8_of(w.z, w.w, fk[j]) : bf16x8_of(w.x, w.y, fk[j]);
+                }
+            };
+            auto read_q = [&](int i, bf16x8 (&q)[RT]) {
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int rt = 0; rt < RT; ++rt) q[rt] = sh.q[rt][i >> 1][i & 1][lane];
+            };
+            constexpr bool kAhead = RT < 4 || !EVEN;  // (else the reads ahead spill: 16 x 8 rows of D = 256, 78 us; 73 so)
+            if (kAhead) read_q(0, qq[0]);
+            half(0, kc[0]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const bf16x8 qq = sh.q[rt][c][e][lane];
-                        s[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0[e], qq, s[rt][0], 0, 0, 0);
-                        s[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1[e], qq, s[rt][1], 0, 0, 0);
+            for (int i = 0; i < 2 * C; ++i) {
+                if (kAhead && i + 1 < 2 * C) read_q(i + 1, qq[(i + 1) & 1]);
+                if (!kAhead) read_q(i, qq[i & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + 1 < 2 * C) half(i + 1, kc[(i + 1) & 1]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    s[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[i & 1][0], qq[i & 1][rt], s[rt][0], 0, 0, 0);
+                    s[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[i & 1][1], qq[i & 1][rt], s[rt][1], 0, 0, 0);
+                }
+                if (RT < 4) {                         // (one product, then its share of the conversions)
+#pragma unroll
+                    for (int k = 0; k < 2 * RT; ++k) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, (8 + 2 * RT - 1) / (2 * RT), 0);
                     }
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
             // the next step's K and scales, then the ids after it (past the last
