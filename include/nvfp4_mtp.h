@@ -480,9 +480,8 @@ int moe_workspace_status(void *workspace, size_t ws_bytes, uint32_t *status, voi
 /* ---- attention of the draft step: rotary positions and an 8-bit cache ----
  *
  * The steps between q|k|v and o in the draft step ([new.rs] `MtpHead::new`
- * resolves `rope_forward`, `reshape_and_cache_flash_fp8` and
- * `paged_decode_attn_fp8`; the pages give no formulas, so the definitions
- * here are the library's own).
+ * resolves handles for them; the pages give no formulas, so the definitions here
+ * are the library's own).
  *
  * Strided rows of heads (host descriptor): element d of head h of row r is
  * data[r * row_stride + h * head_stride + d], strides in elements (a
