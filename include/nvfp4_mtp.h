@@ -622,9 +622,9 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  *               256-byte aligned; nothing to initialise; one call at a time
  *               per workspace.  The size depends only on the host fields of
  *               the descriptors.
- * Scores, softmax statistics and sums in fp32; weights are rounded to bf16
- * for the product with v and for their sum.  What a row does not see never reaches it, NaN
- * included.  The result is the same on every call with the same arguments on
+ * Scores, softmax statistics and sums in fp32 (q k^T and its differences within a
+ * row below 3.4e38); weights are rounded to bf16 for the product with v and for
+ * their sum.  What a row does not see never reaches it, NaN included.  The result is the same on every call with the same arguments on
  * the same device.  One or two launches.
  */
 size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);

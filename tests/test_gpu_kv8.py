@@ -420,6 +420,38 @@ def test_attention_extreme_values():
     check_attention(rng, [1, 3], [130, 500], 16, 8, 2, 128, poke=poke)
 
 
+def check_exact_scores(rng, ns, lens, hq, hk, dim, scale, q_exp=0, k_exp=0):
+    """Scores that are whole numbers times 2^(q_exp + k_exp), exact in fp32, and so
+    far apart under the scale that only a row's largest count: the mean of v over
+    those.  Their weights are exactly 1; fp32 sums of up to L terms are off by (L +
+    64) 2^-24 each, the result by its rounding to bf16."""
+    nv = nvm()
+    cu, table, pages = batch(rng, ns, lens, 16)
+    host = ref.Cache(pages, hk, 16, dim, rng)
+    host.k[:] = ref.e4m3_encode(rng.integers(-2, 3, host.k.shape))
+    host.ks[:] = 127 + k_exp
+    q = rng.integers(-2, 3, (sum(ns), hq, dim)) * 2.0 ** q_exp
+    want, _, _ = ref.attention(q, host, table, cu, lens, scale)
+    got = f64(nv.kv8_attention(bf(q), device_cache(host), seqs(cu, lens, table, max(ns)), scale=scale))
+    top = max(np.abs(host.values(table, b, lens[b])[1]).max() for b in range(len(ns)))
+    tol = 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * 2 * (max(lens) + 64) * 2.0 ** -24 * top
+    assert np.isfinite(got).all() and np.all(np.abs(got - want) <= tol), (scale, np.argwhere(~(np.abs(got - want) <= tol))[:3])
+
+
+@pytest.mark.parametrize("scale", [1e3, 1e9, -1e9, 1e30, -2e38])
+@pytest.mark.parametrize("hq,hk,dim,ns,lens", [(8, 1, 128, [1, 3], [1, 1500]), (16, 2, 256, [5, 1], [700, 130]), (6, 2, 64, [70, 2], [300, 129])])
+def test_attention_large_scales(scale, hq, hk, dim, ns, lens):
+    check_exact_scores(np.random.default_rng(31), ns, lens, hq, hk, dim, scale)
+
+
+@pytest.mark.parametrize("q_exp,k_exp,scale", [(40, 0, None), (20, 20, None), (57, 57, None), (57, 57, -0.5), (50, 57, 1e6), (57, 50, 1e30)])
+def test_attention_large_scores(q_exp, k_exp, scale):
+    """Scores up to 2^124 under ordinary scales, and under scales that take the
+    product past fp32's range."""
+    for hq, hk, dim, ns, lens in ((8, 1, 128, [1, 3], [65, 1500]), (4, 2, 256, [40, 1], [400, 2000])):
+        check_exact_scores(np.random.default_rng(32), ns, lens, hq, hk, dim, dim ** -0.5 if scale is None else scale, q_exp, k_exp)
+
+
 def test_attention_strided_rows():
     nv = nvm()
     rng = np.random.default_rng(24)
