@@ -610,7 +610,8 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  * it after the rows' own k and v are appended.
  *   q           [rows][q_heads][head_dim] head rows; q_heads a multiple of
  *               kv_heads.
- *   scale       any factor (below 2.3e38, times log2(e) finite in fp32);
+ *   scale       any factor (below 2.3e38, times log2(e) finite in fp32; 0: a
+ *               plain mean);
  *               window, sinks >= 0 (sinks without a window changes nothing).
  *   out         bf16, row r head h at out + r * out_row_stride + h * head_dim
  *               (the o projection's activation row), 16-byte aligned,

@@ -64,8 +64,8 @@ struct AttnArgs {
     HeadRows q;
     KV8 c;
     Seqs s;
-    float scale;            // |scale| * log2(e)
-    bool negate;            // scale < 0
+    float scale;            // |scale| * log2(e), 1 for a scale of 0
+    bool negate, zero;      // scale < 0, scale == 0
     int window, sinks;
     uint16_t *out;
     int64_t out_stride;
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
         nid = load_ids(next);
     }
     // Q into LDS (each wavefront a part); a scale below zero is its magnitude on the
-    // negated q
+    // negated q, a scale of zero is any other on q = 0 (what is not finite stays: NaN)
     constexpr int QN = (RT * C * 2 + 3) / 4;
     uint4 qv[QN];
 #pragma unroll
@@ -391,9 +391,13 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
     for (int k = 0; k < QN; ++k) {
         const int f = k * 4 + wave;
         const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        auto prepared = [&](uint32_t w) {
+            if (a.zero) return ((w & 0x7F80u) == 0x7F80u ? w & 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFF0000u : 0u);
+            return w ^ flip;
+        };
         if (f < RT * C * 2)
             (&sh.q[0][0][0][0])[f * 64 + lane] =
-                __builtin_bit_cast(bf16x8, make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip));
+                __builtin_bit_cast(bf16x8, make_uint4(prepared(qv[k].x), prepared(qv[k].y), prepared(qv[k].z), prepared(qv[k].w)));
     }
     __syncthreads();
 
@@ -817,10 +821,10 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
     a.q = view(q);
     a.c = view(cache);
     a.s = view(seqs);
-    // at least the smallest normal number: a hidden score of -inf stays -inf, and any
-    // finite score times it is 0 to exp2
-    a.scale = __builtin_fmaxf(scale2, 1.17549435e-38f);
+    // (a hidden token's score of -inf times a scale of 0 would be NaN)
+    a.scale = scale == 0.0f ? 1.0f : scale2;
     a.negate = scale < 0.0f;
+    a.zero = scale == 0.0f;
     a.window = window;
     a.sinks = sinks;
     a.out = out;

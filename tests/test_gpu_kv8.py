@@ -452,6 +452,30 @@ def test_attention_large_scores(q_exp, k_exp, scale):
         check_exact_scores(np.random.default_rng(32), ns, lens, hq, hk, dim, dim ** -0.5 if scale is None else scale, q_exp, k_exp)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-60, 1e-44, -1e-40, 3e-38])
+def test_attention_scales_near_zero(scale):
+    """A scale of zero is a plain mean whatever the scores; one among the
+    subnormals counts as it is (1e-60 is zero in fp32)."""
+    nv = nvm()
+    rng = np.random.default_rng(33)
+    for hq, hk, dim, ns, lens in ((8, 1, 128, [1, 3], [65, 1500]), (4, 2, 256, [40, 1], [400, 300])):
+        cu, table, pages = batch(rng, ns, lens, 16)
+        host = ref.Cache(pages, hk, 16, dim, rng)
+        host.k[:] = ref.e4m3_encode(rng.integers(-2, 3, host.k.shape))
+        host.ks[:] = 127 + 58
+        q = rng.integers(-2, 3, (sum(ns), hq, dim)) * 2.0 ** 58          # scores up to 2^126
+        want, bound, _ = ref.attention(q, host, table, cu, lens, float(np.float32(scale)))
+        got = f64(nv.kv8_attention(bf(q), device_cache(host), seqs(cu, lens, table, max(ns)), scale=scale))
+        assert np.all(np.abs(got - want) <= bound), scale
+    # zero times what is not finite is NaN, in its row and head alone
+    host.k[table[0, 0], 0, 3, 1] = 0x7F
+    q[40, 3, 5] = np.inf
+    want, bound, _ = ref.attention(q, host, table, cu, lens, 0.0)
+    got = f64(nv.kv8_attention(bf(q), device_cache(host), seqs(cu, lens, table, max(ns)), scale=0.0))
+    nan = np.isnan(want)
+    assert nan.any() and np.array_equal(np.isnan(got), nan) and np.all(np.abs(got - want)[~nan] <= bound[~nan])
+
+
 def test_attention_strided_rows():
     nv = nvm()
     rng = np.random.default_rng(24)
