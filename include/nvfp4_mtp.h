@@ -625,7 +625,9 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  *               the descriptors.
  * Scores, softmax statistics and sums in fp32 (q k^T and its differences within a
  * row below 3.4e38); weights are rounded to bf16 for the product with v and for
- * their sum.  What a row does not see never reaches it, NaN included.  The result is the same on every call with the same arguments on
+ * their sum.  An average of finite values is finite; beside V pages with values
+ * above 2^88, terms below 2^-86 may be lost.  What a row does not see never reaches
+ * it, NaN included.  The result is the same on every call with the same arguments on
  * the same device.  One or two launches.
  */
 size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);

@@ -24,7 +24,7 @@
 // The reference m is common to the four wavefronts and moves only when some score
 // exceeds it by more than kSlack (2^kSlack in the weights): the usual step needs
 // no exchange of maxima, just one barrier for P (double buffered).  Weights up to
-// 2^kSlack cost nothing: bf16 and fp32 keep their relative precision.  m is a score
+// 2^kSlack cost no precision (bf16 and fp32 keep it relative; for range see kLargeV).  m is a score
 // before scaling and a weight 2^((s - m) scale), so that the row's maximum has the
 // weight 1 whatever its size.  (The rounded product m scale subtracted from s scale
 // in one fma leaves half an ulp of it in every exponent, 2^7 from 2^31 on: infinite or
@@ -42,6 +42,13 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 constexpr int kStep = 128;        // tokens a step
 constexpr float kSlack = 6.0f;
+
+// A sum of up to 2^31 weights of up to 2^kSlack each, times V, stays below 2^128 while
+// the pages' exponents are at most 80.  From the first larger one on, a row tile's
+// weights and sums are 2^-kLow of what they would be (its averages come out the same;
+// terms below 2^-86 may be lost then).
+constexpr uint32_t kLargeV = 80 + 127;
+constexpr float kLow = 40.0f, kLowFactor = 0x1p-40f;
 
 // x / d for 0 <= x < 2^31 by a multiplication with a host-made reciprocal: with l =
 // ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1 and t the high word of m x, the
@@ -134,7 +141,8 @@ __device__ __forceinline__ Keys key_range(int pos_lo, int pos_hi, int window, in
     return k;
 }
 
-// Floats of one partial result: 16 rows x D sums (C layout), 16 maxima, 16 sums.
+// Floats of one partial result: 16 rows x D averages (C layout; a sum could pass
+// fp32's range), 16 maxima, 16 sums of weights.
 template <int D>
 constexpr int part_floats() { return 16 * D + 32; }
 
@@ -352,6 +360,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
     f32x4 o[RT][DW];
     float m[RT], l[RT];
     uint32_t poison[RT];              // bit 4 dt + i: o[rt][dt][i] is NaN
+    float low = 0.0f;                 // or kLow
     int step = 0, next = 0;
     Ids id{}, nid{};
     if (v0 < v1) {
@@ -421,7 +430,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
                 bf16x2 p[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    p[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f((s[rt][j][i] - ref) * a.scale));
+                    p[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][j][i] - ref, a.scale, -low)));
                 sum[rt] = dot2(p[0], as_bf16x2(0x3F803F80u), sum[rt]);
                 sum[rt] = dot2(p[1], as_bf16x2(0x3F803F80u), sum[rt]);
                 *reinterpret_cast<uint2 *>(&sh.p[buf][rt * 16 + r][32 * wave + 16 * j + 4 * g]) =
@@ -534,6 +543,24 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) l[rt] += sum[rt];
             const float fv[2] = {kv8_scale(sv[0]), kv8_scale(sv[1])};
+            // (every wavefront has all of the step's scales of V)
+            if (low == 0.0f && __any(max(sv[0], sv[1]) > kLargeV)) {
+                low = kLow;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    l[rt] *= kLowFactor;
+#pragma unroll
+                    for (int dt = 0; dt < DW; ++dt) o[rt][dt] *= kLowFactor;
+                }
+                // and the wavefront's weights of this step
+#pragma unroll 1
+                for (int k = 0; k < 2 * RT; ++k) {
+                    uint16_t *p = &sh.p[buf][(k >> 1) * 16 + r][32 * wave + 16 * (k & 1) + 4 * g];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = (uint16_t)f32_to_bf16_bits(bf16_bits_to_f32(p[i]) * kLowFactor);
+                }
+                __syncthreads();
+            }
             if (!whole) {
                 // A token that some row does not see may hold a NaN in V that the row
                 // must not get (0 * NaN is NaN): such codes are counted per (dim, row)
@@ -625,9 +652,11 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
         for (int rt = 0; rt < RT; ++rt) {
             if (row0 + rt * 16 + r >= rows) continue;
             float *p = part_at(blockIdx.x * 2 + slot, rt);
+            const float inv = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
 #pragma unroll
-            for (int dt = 0; dt < DW; ++dt) *reinterpret_cast<f32x4 *>(p + (wave * DW + dt) * 256 + lane * 4) = o[rt][dt];
-            if (threadIdx.x < 16) *reinterpret_cast<float2 *>(p + 16 * D + 2 * r) = make_float2(m[rt], l[rt]);
+            for (int dt = 0; dt < DW; ++dt) *reinterpret_cast<f32x4 *>(p + (wave * DW + dt) * 256 + lane * 4) = o[rt][dt] * inv;
+            if (threadIdx.x < 16)
+                *reinterpret_cast<float2 *>(p + 16 * D + 2 * r) = make_float2(m[rt], low == 0.0f ? l[rt] : l[rt] * (1.0f / kLowFactor));
         }
         continue;
     }
@@ -663,7 +692,7 @@ __global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int grid) {
     if (row >= rows) return;
     float mx = -INFINITY, sum = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    // n pieces at a time, their loads in flight together
+    // n pieces at a time, their loads in flight together; o stays an average
     auto add = [&](auto n) {
         constexpr int N = decltype(n)::value;
         for (int k0 = 0; k0 < pieces.count; k0 += N) {
@@ -675,15 +704,22 @@ __global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int grid) {
                 ml[k] = *reinterpret_cast<const float2 *>(p + 16 * D + 2 * r);
                 v[k] = *reinterpret_cast<const f32x4 *>(p + dt * 256 + lane * 4);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            float mn = mx;
+#pragma unroll
+            for (int k = 0; k < N; ++k) mn = fmaxf(mn, ml[k].x);
+            const float ref = mn == -INFINITY ? 0.0f : mn, old = sum * __builtin_amdgcn_exp2f((mx - ref) * a.scale);
+            sum = old;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                if (k0 + k >= pieces.count) continue;
-                const float mn = fmaxf(mx, ml[k].x), ref = mn == -INFINITY ? 0.0f : mn;
-                const float fa = __builtin_amdgcn_exp2f((mx - ref) * a.scale), fb = __builtin_amdgcn_exp2f((ml[k].x - ref) * a.scale);
-                sum = sum * fa + ml[k].y * fb;
-                o = o * fa + v[k] * fb;
-                mx = mn;
+                ml[k].y = k0 + k < pieces.count ? ml[k].y * __builtin_amdgcn_exp2f((ml[k].x - ref) * a.scale) : 0.0f;
+                sum += ml[k].y;
             }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            o *= old * inv;
+#pragma unroll
+            for (int k = 0; k < N; ++k) o += v[k] * (ml[k].y * inv);
+            mx = mn;
         }
     };
     // (one token over 1500 keys, 12 pieces: 12.6 us eight at a time, 11.9 sixteen; a
@@ -694,7 +730,7 @@ __global__ __launch_bounds__(64) void k_attn_join(AttnArgs a, int grid) {
         add(std::integral_constant<int, 16>{});
     const int i = a.group.div(row), hq = h * (int)a.group.d + row - i * (int)a.group.d;
     store_out(a.out + (int64_t)(sq.r0 + i) * a.out_stride + (int64_t)hq * D + dt * 16 + 4 * (lane >> 4),
-              o * (sum == 0.0f ? 0.0f : 1.0f / sum));
+              o);
 }
 
 struct AttnPlan {

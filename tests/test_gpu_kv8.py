@@ -476,6 +476,49 @@ def test_attention_scales_near_zero(scale):
     assert nan.any() and np.array_equal(np.isnan(got), nan) and np.all(np.abs(got - want)[~nan] <= bound[~nan])
 
 
+@pytest.mark.parametrize("hq,hk,dim,ns,lens", [(8, 1, 128, [1, 3], [2, 1500]), (16, 2, 256, [1], [9001]), (16, 2, 256, [5, 6], [700, 40]),
+                                               (4, 2, 64, [100, 2], [300, 129])])
+@pytest.mark.parametrize("flat", [False, True])
+def test_attention_large_values_in_sight(hq, hk, dim, ns, lens, flat):
+    """V up to the largest value the cache holds, of one sign, in every page or
+    in some: an average of finite values is finite."""
+    def poke(host, table, q):
+        if flat:
+            q[:] = 0.0
+        host.v[:] = host.v & 0x7F
+        host.vs[:] = 246
+    rng = np.random.default_rng(34)
+    got = check_attention(rng, ns, lens, 16, hq, hk, dim, poke=poke)
+    assert np.isfinite(got).all() and np.abs(got).max() > 1e37
+
+    def late(host, table, q):                         # small values, then large ones, then small ones
+        if flat:
+            q[:] = 0.0
+        host.vs[table[:, table.shape[1] // 2]] = 246
+        host.vs[table[0, -1]] = 208
+    check_attention(rng, ns, lens, 16, hq, hk, dim, poke=late)
+
+    def hidden(host, table, q):                       # large values that a window hides: the small ones keep their precision
+        host.vs[table[:, 0]] = 246
+    check_attention(rng, ns, lens, 16, hq, hk, dim, window=20, poke=hidden)
+
+
+def test_attention_largest_value_of_many():
+    """Equal keys, every visible value the largest: the average is that value."""
+    nv = nvm()
+    rng = np.random.default_rng(35)
+    for rows, length in ((1, 20000), (2, 3), (300, 1000)):
+        cu, table, pages = batch(rng, [rows], [length], 64)
+        host = ref.Cache(pages, 2, 64, 128, rng)
+        host.k[:], host.v[:], host.vs[:] = 0x38, 0x7E, 246
+        q = normal(rng, (rows, 8, 128))
+        got = f64(nv.kv8_attention(bf(q), device_cache(host), seqs(cu, [length], table, rows)))
+        want = 448.0 * 2.0 ** 119
+        # equal weights cancel up to fp32 sums of up to `length` terms
+        seen = (np.arange(rows) + length - rows >= 0)
+        assert np.all(np.abs(got[seen] - want) <= want * (2.0 ** -8 + 2 * (length + 64) * 2.0 ** -24)), (rows, length)
+
+
 def test_attention_strided_rows():
     nv = nvm()
     rng = np.random.default_rng(24)
