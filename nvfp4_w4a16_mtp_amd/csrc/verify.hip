@@ -242,12 +242,16 @@ __global__ __launch_bounds__(kVThreads) void k_verify_stats(VerifyArgs a, int ki
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum += term_above(x[g][j], ref, low, it);
         } else {
-            const float c = (float)fmin(it, 3.0e38);
+            // (finite logits can be 6.8e38 apart, which temperatures near that make count:
+            // half the difference, exact, times 2 c)
+            float c = (float)fmin(it, 3.0e38);
+            const float h = c < 0x1p-100f ? 0.5f : 1.0f, shift = -ref * h;
+            c /= h;
             float part = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f((x[g][j] - ref) * c);
+                for (int j = 0; j < E; ++j) part += __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][j], h, shift) * c);
             sum = part;
         }
         for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_f64(sum, m);

@@ -157,6 +157,24 @@ def test_verify_far_from_zero(vocab, batch, sampled):
     check(logits, cu, ids, ua * 0.3, us, temp=temp, draft=draft if sampled else None)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,batch", [(3000, 3), (20011, 60)])
+def test_verify_logits_further_apart_than_fp32_holds(vocab, batch, dtype):
+    """Finite logits at both ends of fp32 under temperatures that let both count:
+    a sum without the lower ones would be about half, and random numbers 1.3 times
+    p(d) would let drafts stand."""
+    rng = np.random.default_rng(vocab + 1)
+    rows = 3 * batch
+    logits = np.where(rng.random((rows, vocab)) < 0.1, 3.3e38, -3.3e38) * rng.uniform(0.9, 1.0, (rows, vocab))
+    logits = torch.from_numpy(np.float32(logits)).to(dtype).double().numpy()
+    ids = logits.argmax(1)
+    temp = np.float32(rng.choice([2.5e38, 3e38, 3.4e38], batch))
+    p = np.array([1 / ref.softmax(logits[r], float(temp[r // 3]))[1] for r in range(rows)])
+    ua = p * np.where(np.arange(rows) % 3 == 0, 0.7, 1.3)
+    out = check(logits, np.arange(0, rows + 1, 3), ids, ua, rng.random(batch), temp=temp, dtype=dtype)
+    assert np.all(out[0] == 1)
+
+
 def test_verify_temperatures():
     rng = np.random.default_rng(6)
     cu, logits, draft, ids, ua, us = make(rng, [3] * 8, 2000)
