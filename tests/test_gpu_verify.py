@@ -188,6 +188,67 @@ def test_verify_temperatures():
         assert out[0][1] >= 1 and out[0][2] == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sampled", [False, True])
+@pytest.mark.parametrize("batch,vocab,most", [(56, 151936, 4), (300, 33003, 3)])
+def test_verify_large_batches(batch, vocab, most, sampled, dtype):
+    """Rows and sequences enough that a wavefront takes a chunk alone, in the first
+    pass and in the second."""
+    rng = np.random.default_rng(batch)
+    ns = [int(x) for x in rng.integers(1, most + 1, batch)]
+    ns[batch // 2] = 0
+    cu, logits, draft, ids, ua, us = make(rng, ns, vocab, peak=4.0)
+    temp = rng.choice([0.4, 0.7, 1.0, 0.0], batch)
+    out = check(logits, cu, ids, ua * 0.5, us, temp=temp, draft=draft if sampled else None, lens=rng.integers(10, 1000, batch), dtype=dtype)
+    assert 0 < out[0].sum() < sum(ns) - batch
+
+
+def check_next_to_the_border(batch, vocab, sampled, dtype, of_draft):
+    """u_accept 2^-17 to 2^-22 of it below, at and above min(p(d) / q(d), 0.999).
+    Drafts: the target's first choices, or the draft model's."""
+    rng = np.random.default_rng(vocab)
+    cu, logits, draft, ids, ua, us = make(rng, [2] * batch, vocab, peak=2.0)
+    ids = (draft if of_draft else logits).argmax(1)
+    temp = np.float32(rng.uniform(0.5, 1.5, batch))
+
+    def seen(x):
+        return torch.from_numpy(np.float32(x)).to(dtype).double().numpy()
+    ua = np.zeros(2 * batch, np.float32)
+    want = []
+    for b in range(batch):
+        (e, total), d = ref.softmax(seen(logits[2 * b]), float(temp[b])), ids[2 * b]
+        border = e[d] / total
+        if sampled:
+            e, total = ref.softmax(seen(draft[2 * b]), float(temp[b]))
+            border /= e[d] / total
+        near = np.float32(min(border, 0.999) * (1 + [0.0, 1.0, -1.0][b % 3] * 2.0 ** -rng.integers(17, 23)))
+        # the oracle's and the kernel's fp64 sums are off by less than 1e-11 relative
+        while abs(float(near) / border - 1) < 1e-10:
+            near = np.nextafter(near, np.float32(0))
+        ua[2 * b] = near
+        want.append(int(float(near) < border))
+    out = check(logits, cu, ids, ua, us, temp=temp, draft=draft if sampled else None, dtype=dtype)
+    assert np.array_equal(out[0], want)
+    return want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sampled", [False, True])
+@pytest.mark.parametrize("batch,vocab", [(6, 5000), (70, 20011), (300, 33003)])
+def test_verify_random_numbers_next_to_the_border(batch, vocab, sampled, dtype):
+    """Closer to the border than fp32 sums can tell."""
+    want = check_next_to_the_border(batch, vocab, sampled, dtype, False)
+    if not sampled:                                   # (a draft model that finds them less likely: they stand)
+        assert 0 < sum(want) < batch
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch,vocab", [(70, 20011), (300, 33003)])
+def test_verify_sampled_random_numbers_next_to_the_border(batch, vocab, dtype):
+    want = check_next_to_the_border(batch, vocab, True, dtype, True)
+    assert 0 < sum(want) < batch
+
+
 def test_verify_rows_bounds_and_aliasing():
     nv = nvm()
     rng = np.random.default_rng(7)
