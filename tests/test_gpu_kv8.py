@@ -353,6 +353,55 @@ def test_attention_prompt(hq, hk, dim):
     check_attention(rng, [130, 1, 67], [130, 300, 200], 16, hq, hk, dim)
 
 
+@pytest.mark.parametrize("hq,hk,dim,ns", [(16, 2, 256, [5, 6, 1]), (16, 2, 128, [6, 5, 2]), (12, 2, 192, [8, 6, 1]), (16, 2, 192, [8, 7, 1]),
+                                          (16, 2, 64, [5, 1, 6]), (16, 2, 256, [8, 7, 2])])
+@pytest.mark.parametrize("P", [16, 128])
+def test_attention_three_and_four_row_tiles(hq, hk, dim, ns, P):
+    """33 to 64 rows a kv head, keys split over workgroups and not."""
+    rng = np.random.default_rng(hq + dim + P)
+    check_attention(rng, ns, [700, 1300, 130], P, hq, hk, dim)
+    check_attention(rng, ns, [9, 6, 3000], P, hq, hk, dim, window=200, sinks=3)
+
+
+@pytest.mark.parametrize("count", [64, 65, 257, 300, 1024, 1025])
+@pytest.mark.parametrize("hq,dim,most", [(16, 64, 1), (8, 128, 4), (16, 64, 3), (4, 192, 2), (16, 256, 2)])
+def test_attention_many_sequences(count, hq, dim, most):
+    """Sequences in several wavefronts' and several rounds' prefix sums, and more
+    than share their steps evenly; some without rows or without tokens."""
+    rng = np.random.default_rng(count + dim + most)
+    ns = rng.integers(0, most + 1, count)
+    ns[-1] = most
+    lens = np.where(rng.random(count) < 0.1, 0, rng.integers(1, 200, count))
+    lens[count // 3], lens[-1] = 1500, 700
+    check_attention(rng, [int(n) for n in ns], [int(x) for x in lens], 16, hq, 1, dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("n", [1, 20, 40])
+def test_attention_wide_block_table(dim, n):
+    """A block table of so many steps that they are not shared evenly: keys in
+    pieces, one to three row tiles."""
+    nv = nvm()
+    rng = np.random.default_rng(dim + n)
+    heads = 512 if dim <= 128 else 256
+    length = 300
+    host = ref.Cache(4, heads, 128, dim, rng)
+    table = np.array([[2, 0, 3]], np.int32)
+    wide = torch.zeros((1, (1 << 30) // heads), dtype=torch.int32, device="cuda")
+    wide[:, :3] = i32(table)
+    q = normal(rng, (n, heads, dim))
+    want, bound, _ = ref.attention(q, host, table, [0, n], [length], dim ** -0.5)
+    s = nv.KV8Seqs(i32([0, n]), i32([length]), wide, max_rows=n, max_kv_len=length)
+    got = f64(nv.kv8_attention(bf(q), device_cache(host), s))
+    assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("hq,hk,dim", [(16, 2, 256), (8, 1, 128)])
+def test_attention_prompt_chunk_beside_decode_rows(hq, hk, dim):
+    rng = np.random.default_rng(dim)
+    check_attention(rng, [1, 150, 1, 0, 2, 1], [3000, 400, 1, 9, 129, 800], 16, hq, hk, dim)
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (17, 3), (64, 64), (100, 65), (128, 4), (5000, 4), (300, 1000)])
 def test_attention_window(window, sinks):
     rng = np.random.default_rng(window + sinks)
