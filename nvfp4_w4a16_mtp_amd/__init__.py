@@ -678,6 +678,13 @@ def _int32(t: torch.Tensor, name: str):
         raise TypeError(f"{name} must be int32")
 
 
+def _fits32(v: int, name: str) -> int:
+    """A host integer for the library's int32 (ctypes would cut it)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name}={v} does not fit 32 bits")
+    return v
+
+
 def _same_device(index: int, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != index:
@@ -748,6 +755,8 @@ class KV8Seqs:
 
     def __post_init__(self):
         batch = self.kv_lens.numel()
+        _fits32(self.max_rows, "max_rows")
+        _fits32(self.max_kv_len, "max_kv_len")
         for t, name in ((self.cu_rows, "cu_rows"), (self.kv_lens, "kv_lens"), (self.block_table, "block_table")):
             _int32(t, name)
         if self.cu_rows.numel() != batch + 1 or self.block_table.dim() != 2 or self.block_table.shape[0] != batch:
@@ -761,7 +770,7 @@ class KV8Seqs:
         ref = self._refs.get(rows)
         if ref is None:
             d = _KV8Seqs(self.cu_rows.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(), self.kv_lens.numel(),
-                         rows, self.max_rows, self.block_table.shape[1], self.max_kv_len)
+                         _fits32(rows, "rows"), self.max_rows, self.block_table.shape[1], self.max_kv_len)
             if len(self._refs) >= 64:
                 self._refs.clear()
             ref = self._refs[rows] = ctypes.byref(d)
@@ -815,7 +824,7 @@ def rope_qk(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Ten
     (either may be None; rows and heads may be strided).  Returns (q_out,
     k_out); pass q_out=q to rotate in place."""
     _int32(positions, "positions")
-    rows, index, byref = positions.numel(), positions.get_device(), ctypes.byref
+    rows, index, byref = _fits32(positions.numel(), "rows"), positions.get_device(), ctypes.byref
     dq = dqo = dk = dko = None
     if q is not None:
         if q_out is None:
@@ -898,6 +907,7 @@ def kv8_read(cache: KV8Cache, seqs: KV8Seqs, rows: int | None = None, k_out: tor
 
 def kv8_attention_workspace(cache: KV8Cache, seqs: KV8Seqs, q_heads: int, rows: int) -> torch.Tensor:
     """Workspace for kv8_attention of `rows` rows (nothing to initialise)."""
+    _fits32(q_heads, "q_heads")
     with torch.cuda.device(cache.index):
         nbytes = lib().kv8_attention_workspace_bytes(cache._ref, seqs._ref(rows), q_heads)
     if nbytes == 0:
@@ -921,7 +931,7 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float 
     _dev(workspace, "workspace")
     _same_device(index, q, out, workspace, seqs.kv_lens)
     _run("kv8_attention", lib().kv8_attention, index, ctypes.byref(dq), cache._ref, seqs._ref(q.shape[0]),
-         dq.dim ** -0.5 if scale is None else scale, window, sinks, do.data, do.row_stride, workspace.data_ptr(),
+         dq.dim ** -0.5 if scale is None else scale, _fits32(window, "window"), _fits32(sinks, "sinks"), do.data, do.row_stride, workspace.data_ptr(),
          workspace.nbytes)
     return out
 
@@ -938,6 +948,8 @@ class Verified(NamedTuple):
 
 def verify_workspace(max_rows: int, batch: int, vocab: int, device, sampled: bool = False) -> torch.Tensor:
     """Workspace for verify_drafts (nothing to initialise)."""
+    for v, name in ((max_rows, "max_rows"), (batch, "batch"), (vocab, "vocab")):
+        _fits32(v, name)
     with torch.cuda.device(device):
         nbytes = lib().verify_drafts_workspace_bytes(batch, max_rows, vocab, int(sampled))
     if nbytes == 0:
@@ -966,6 +978,7 @@ def verify_drafts(logits: torch.Tensor, cu_rows: torch.Tensor, draft_ids: torch.
     if not logits.is_cuda:
         raise ValueError("logits must be a device tensor")
     index, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    _fits32(max_rows, "max_rows")
     rows, vocab = logits.shape
     batch = cu_rows.numel() - 1
     strides = []

@@ -568,6 +568,32 @@ def test_attention_largest_value_of_many():
         assert np.all(np.abs(got[seen] - want) <= want * (2.0 ** -8 + 2 * (length + 64) * 2.0 ** -24)), (rows, length)
 
 
+def test_host_integers_past_32_bits_are_refused():
+    """None is cut to its low bits: a window of 2^32 is not no window."""
+    nv = nvm()
+    rng = np.random.default_rng(36)
+    dev = device_cache(ref.Cache(2, 1, 16, 64, rng))
+    q = bf(rng.normal(0, 1, (1, 1, 64)))
+    args = (i32([0, 1]), i32([20]), i32([[0, 1]]))
+    s = nv.KV8Seqs(*args, max_rows=1)
+    for v in (1 << 32, (1 << 32) + 1, 1 << 31, -(1 << 31) - 1):
+        for kw in (dict(window=v), dict(window=5, sinks=v)):
+            with pytest.raises(ValueError):
+                nv.kv8_attention(q, dev, s, **kw)
+        for kw in (dict(max_rows=v), dict(max_rows=1, max_kv_len=v)):
+            with pytest.raises(ValueError):
+                nv.KV8Seqs(*args, **kw)
+        with pytest.raises(ValueError):
+            nv.kv8_attention_workspace(dev, s, v, 1)
+        with pytest.raises(ValueError):
+            nv.kv8_attention_workspace(dev, s, 1, v)
+        with pytest.raises(ValueError):
+            nv.verify_workspace(v, 1, 10, "cuda")
+        with pytest.raises(ValueError):
+            nv.verify_drafts(torch.zeros((1, 10), device="cuda"), i32([0, 1]), i32([0]), torch.zeros(1, device="cuda"),
+                             torch.zeros(1, device="cuda"), v)
+
+
 def test_attention_strided_rows():
     nv = nvm()
     rng = np.random.default_rng(24)
