@@ -20,6 +20,11 @@ int check_launch(const char *what);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A launch of one dimension: fewer than 2^32 threads, fewer than 2^31 workgroups.
+inline bool grid_fits(int64_t blocks, int threads) {
+    return blocks <= 2147483647LL && blocks <= 4294967295LL / threads;
+}
+
 int validate_weight(const nvfp4_weight *w, const char *what);
 
 // Number of compute units of the current device (cached per device).

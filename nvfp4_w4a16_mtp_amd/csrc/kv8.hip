@@ -549,7 +549,7 @@ extern "C" int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, c
     const int per = heads_per_thread((int64_t)rows * units, tq.heads + tk.heads);
     const int qg = (tq.heads + per - 1) / per, kg = (tk.heads + per - 1) / per;
     const int64_t blocks = ((int64_t)rows * units + 255) / 256;
-    if (blocks > 2147483647LL || qg + kg > 65535) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!grid_fits(blocks, 256) || qg + kg > 65535) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     const Rope rp{rope->inv_freq, rope->rot_dim, rope->interleaved != 0, rope->mscale};
     hipLaunchKernelGGL(k_rope, dim3((unsigned)blocks, qg + kg), dim3(256), 0, reinterpret_cast<hipStream_t>(stream), tq,
                        tk, rp, positions, rows, uq > 0 ? uq : 1, uk > 0 ? uk : 1, per, qg);
@@ -595,7 +595,7 @@ static int append(const char *who, const nvfp4_kv8_cache *cache, const nvfp4_kv8
         a.q_groups = (tq.heads + a.q_per - 1) / a.q_per;
         blocks += (units + threads - 1) / threads * a.q_groups;
     }
-    if (blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!grid_fits(blocks, threads)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     a.kv_blocks = (int)kv_blocks;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (rope) {
@@ -648,7 +648,7 @@ extern "C" int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs
     a.items = (int)(((int64_t)max_rows + 2 * P - 2) / P);
     a.lists = k_out && v_out ? 2 : 1;
     const int64_t blocks = (int64_t)seqs->batch * a.items * a.lists * cache->kv_heads;
-    if (blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!grid_fits(blocks, 256)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     hipLaunchKernelGGL(k_kv8_read, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<hipStream_t>(stream), a);
     return check_launch(who);
 }

@@ -849,7 +849,7 @@ extern "C" int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *ca
         return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_rows=%d rows of %d query heads a kv head are too many", who, seqs->max_rows,
                     q->heads / cache->kv_heads);
     const AttnPlan p = attn_plan(cache, seqs, q->heads);
-    if (p.blocks > 2147483647LL || p.join_blocks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!grid_fits(p.blocks, 256) || !grid_fits(p.join_blocks, 64)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     if (!workspace || ws_bytes < p.ws)
         return fail(NVFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : 0, p.ws);
     if (!aligned(workspace, 256)) return fail(NVFP4_ERR_ALIGN, "%s: workspace not 256-byte aligned", who);

@@ -752,7 +752,8 @@ extern "C" int verify_drafts(const void *logits, int32_t logits_dtype, int64_t r
     if (!workspace || ws_bytes < p.ws + 16)
         return fail(NVFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : 0, p.ws + 16);
     if (!aligned(workspace, 16)) return fail(NVFP4_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
-    if ((int64_t)batch * max_rows * 2 * p.chunks > 2147483647LL) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    if (!grid_fits((int64_t)batch * max_rows * (draft_logits ? 2 : 1) * (p.many ? (p.chunks + 3) / 4 : p.chunks), kVThreads))
+        return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
     VerifyArgs a;
     a.logits = logits;
     a.draft = draft_logits;

@@ -235,6 +235,25 @@ def test_other_refusals():
     assert L.verify_drafts_workspace_bytes(2, 65, 100, 0) == 0
 
 
+@built
+def test_grids_past_32_bits_of_threads_are_refused():
+    """By the host's own check, before anything is launched."""
+    import nvfp4_w4a16_mtp_amd as nv
+    L = nv.lib()
+    B = ctypes.byref
+    big = 2 ** 31 - 1
+    c, s, r, rp = _cache(nv), _seqs(nv, batch=big, rows=big, max_rows=64), _rows(nv), nv._Rope(4096, 32, 0, 1.0)
+    one = _rows(nv, heads=1)
+    assert L.rope_qk(B(one), B(one), None, None, big, A, B(rp), None) == -5 and b"too large" in L.nvfp4_mtp_last_error()
+    for rows in (big, (1 << 23)):                     # past 2^31 workgroups, and past 2^32 threads alone
+        s = _seqs(nv, batch=rows, rows=rows, max_rows=2)
+        assert L.kv8_append(B(c), B(s), B(r), B(r), None) == -5, rows
+        assert L.rope_kv8_append(B(c), B(s), B(rp), B(r), B(r), B(r), B(r), None) == -5, rows
+        assert L.kv8_read(B(c), B(s), B(r), B(r), None) == -5, rows
+        assert L.kv8_attention(B(r), B(c), B(s), 0.125, 0, 0, A, 128, A, 1 << 62, None) == -5, rows
+    assert L.verify_drafts(A, 0, 151936, 151936, None, 0, A, 1 << 14, 1 << 14, 64, A, None, A, A, None, A, A, A, None, A, 1 << 62, None) == -5
+
+
 def test_frequencies_refuse():
     import nvfp4_w4a16_mtp_amd as nv
     for kw in (dict(rot_dim=24), dict(rot_dim=0), dict(rot_dim=32, base=0.0), dict(rot_dim=32, factor=0.5),
