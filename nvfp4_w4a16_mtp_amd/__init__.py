@@ -799,11 +799,14 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     inv_freq is float64 on `device`."""
     if rot_dim < 16 or rot_dim % 16:
         raise ValueError("rot_dim must be a positive multiple of 16")
-    if not base > 0 or not factor >= 1 or not high_turns > low_turns:
-        raise ValueError("need base > 0, factor >= 1 and high_turns > low_turns")
+    if not 0 < base < math.inf or not 1 <= factor < math.inf or not original_len > 0 or \
+            not -math.inf < low_turns < high_turns < math.inf:
+        raise ValueError("need base > 0, factor >= 1, original_len > 0 and high_turns > low_turns, all finite")
     if scaling not in (None, "linear", "base", "by_parts"):
         raise ValueError(f"unknown scaling {scaling!r}")
     if scaling == "base":
+        if math.log(base) + math.log(factor) * rot_dim / (rot_dim - 2) > 709.0:
+            raise ValueError("the stretched base passes the range of fp64")
         base = base * factor ** (rot_dim / (rot_dim - 2))
     i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
     f = torch.exp(-math.log(base) * i / rot_dim)

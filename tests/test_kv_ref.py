@@ -262,6 +262,21 @@ def test_frequencies_refuse():
             nv.rope_frequencies(device="cpu", **kw)
 
 
+def test_frequencies_refuse_what_is_not_finite():
+    import nvfp4_w4a16_mtp_amd as nv
+    inf, nan = float("inf"), float("nan")
+    for kw in (dict(base=inf), dict(base=nan), dict(factor=inf, scaling="linear"), dict(factor=nan, scaling="base"),
+               dict(scaling="by_parts", original_len=0), dict(scaling="by_parts", original_len=nan),
+               dict(scaling="by_parts", high_turns=inf), dict(scaling="by_parts", low_turns=-inf), dict(scaling="by_parts", low_turns=nan)):
+        with pytest.raises(ValueError):
+            nv.rope_frequencies(32, device="cpu", **kw)
+    for factor in (1e8, 1e300):                       # the stretched base is past fp64's range
+        with pytest.raises(ValueError):
+            nv.rope_frequencies(32, 1e300, scaling="base", factor=factor, device="cpu")
+    f, _ = nv.rope_frequencies(32, 1e290, scaling="base", factor=1e8, device="cpu")
+    assert torch.isfinite(f).all()
+
+
 @built
 def test_bindings_refuse_host_tensors_and_types():
     import nvfp4_w4a16_mtp_amd as nv
