@@ -565,9 +565,10 @@ int rope_qk(const nvfp4_head_rows *q, const nvfp4_head_rows *q_out, const nvfp4_
  *   k, v   [rows][kv_heads][head_dim] head rows.
  * Per page and head, over the tokens of the page that this call writes: amax =
  * max of the finite |x|; e = the smallest exponent >= -110 with amax <= 448 *
- * 2^e, 119 at most (values above 448 * 2^119 = 2.98e38 saturate).  A page that the call writes from its first token on takes e; a page it
- * continues takes max(e, its present exponent), and when that grows the page's
- * earlier codes are re-rounded to it.  code = E4M3 nearest to x * 2^-e (ties
+ * 2^e, 119 at most (values above 448 * 2^119 = 2.98e38 saturate).  A page that
+ * the call writes from its first token on takes e; a page it continues takes
+ * max(e, its present exponent), and when that grows the page's earlier codes are
+ * re-rounded to it.  code = E4M3 nearest to x * 2^-e (ties
  * to even, saturating at 448; infinities saturate, NaN stays NaN).  Powers of
  * two leave every kept value exact unless it falls among the subnormals.
  * Writing the same rows again gives the same page.  After a shortened
@@ -627,8 +628,10 @@ int kv8_read(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, const nvf
  * row below 3.4e38); weights are rounded to bf16 for the product with v and for
  * their sum.  An average of finite values is finite; beside V pages with values
  * above 2^88, terms below 2^-86 may be lost.  What a row does not see never reaches
- * it, NaN included.  The result is the same on every call with the same arguments on
- * the same device.  One or two launches.
+ * it, NaN included.  The result is the same on every call with the same arguments
+ * on the same device.  One or two launches.  Where a sequence has more than 64 rows
+ * a kv head, row tiles and key splits go by that sequence: single rows over long
+ * caches are faster in a call of their own than beside a prompt chunk.
  */
 size_t kv8_attention_workspace_bytes(const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, int32_t q_heads);
 int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const nvfp4_kv8_seqs *seqs, float scale,

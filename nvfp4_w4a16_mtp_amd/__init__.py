@@ -921,8 +921,9 @@ def kv8_attention_workspace(cache: KV8Cache, seqs: KV8Seqs, q_heads: int, rows: 
 def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float | None = None, window: int = 0,
                   sinks: int = 0, workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """Attention of q, bf16 [rows][q_heads][head_dim], over the cache (scale:
-    head_dim^-0.5 by default).  out: bf16 [rows][q_heads][head_dim], heads
-    contiguous."""
+    head_dim^-0.5 by default; 0: a plain mean).  out: bf16
+    [rows][q_heads][head_dim], heads contiguous.  Prompt chunks and single rows
+    over long caches are faster in two calls than in one."""
     dq, index = _rows(q, "q"), cache.index
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)

@@ -24,14 +24,17 @@
 // The reference m is common to the four wavefronts and moves only when some score
 // exceeds it by more than kSlack (2^kSlack in the weights): the usual step needs
 // no exchange of maxima, just one barrier for P (double buffered).  Weights up to
-// 2^kSlack cost no precision (bf16 and fp32 keep it relative; for range see kLargeV).  m is a score
-// before scaling and a weight 2^((s - m) scale), so that the row's maximum has the
-// weight 1 whatever its size.  (The rounded product m scale subtracted from s scale
+// 2^kSlack cost no precision (bf16 and fp32 keep it relative; for range see kLargeV).
+// m is a score before scaling and a weight 2^((s - m) scale), so that the row's maximum
+// has the weight 1 whatever its size.  (The rounded product m scale subtracted from s scale
 // in one fma leaves half an ulp of it in every exponent, 2^7 from 2^31 on: infinite or
 // vanishing rows.  It takes one instruction less a score: prompt chunks 374 us, 382 so.)
 //
 // P is rounded to bf16 (2^-8 relative at most) for the matrix cores, and the row's
-// sum is of the rounded values: a row with one large weight comes out exact.
+// sum is of the rounded values: a row with one large weight comes out exact.  Against
+// 64 bits the relative error (root mean square) is 0.0020 to 0.0023, and 0.0017 with
+// fp32 weights, which is the result's own rounding; weights in two bf16 parts would
+// double the second product.
 #include <type_traits>
 
 #include "kv8.hpp"
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
     };
     uint4 kf[2][C], vf[2][DW];
     uint32_t sk[2], sv[2];
-    auto load_k = [&](int step, const Ids &id) {
+    auto load_k = [&](const Ids &id) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int64_t at = (int64_t)(valid(id.k[j]) ? id.k[j] : 0) * a.c.heads + h;
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
             sk[j] = a.c.ks[at];
         }
     };
-    auto load_v = [&](int step, const Ids &id) {
+    auto load_v = [&](const Ids &id) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int64_t at = (int64_t)(valid(id.v[j]) ? id.v[j] : 0) * a.c.heads + h;
@@ -382,8 +385,8 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
                                                  32 * ce - 24 * (ce & 1));
     }
     if (v0 < v1) {
-        load_k(step, id);
-        load_v(step, id);
+        load_k(id);
+        load_v(id);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -491,7 +494,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
             // step the last one is loaded again)
             step = next;
             const Ids vid = nid;
-            load_k(step, nid);
+            load_k(nid);
             next = keys.step(min(v + 2, v1 - 1));
             nid = load_ids(next);
             __builtin_amdgcn_sched_barrier(0);
@@ -624,7 +627,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
                     }
                 }
             id = vid;
-            load_v(step, id);
+            load_v(id);
             __builtin_amdgcn_sched_barrier(0);
         }
     }

@@ -1,12 +1,20 @@
 // verify_drafts: acceptance of drafted tokens and the token after them
 // (definition in nvfp4_mtp.h).
 //
-// The logits are read once: a chunk of a row gives its maximum, the sum of
-// exp((l - max) / T) and its first maximum's index.  Everything after that works
-// on those partials, and only the one chunk that holds the drawn token is read
-// again.  Bytes bound it for many rows, launches and dependent loads for few.
+// A first pass over the logits gives for every chunk of a row its maximum, the sum of
+// exp((l - max) / T) and, for greedy sequences, its first maximum's index.  Then one of
+// two plans (verify_plan):
+// - few rows of outright drafts, two launches: fp64 sums, without the draft's own
+//   term; the second launch decides and draws from them and reads only the drafts'
+//   logits and the chunk that holds the drawn token again;
+// - else four: the decision; a second pass over the drawn rows (and the draft model's)
+//   for the fp64 sums of what is drawn from; the draw and its chunk.  The first pass of
+//   many outright drafts has fp32 sums, and a test too close for those is made again
+//   with the row's fp64 sum.
+// A row without a softmax is read again for its first maximum.  Bytes bound it for many
+// rows, launches and dependent loads for few.
 //
-// Why fp64.  The drawn token is where a running sum over the vocabulary passes
+// Why fp64 where a token is drawn.  It is where a running sum over the vocabulary passes
 // u * total.  A relative error e of the sums moves every one of V borders, so a
 // draw changes with a probability up to about V * e: a few per cent in fp32 (V =
 // 150000), 1e-7 with the exponential below.  gfx950 runs fp64 FMAs at the fp32
