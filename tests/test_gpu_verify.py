@@ -310,6 +310,72 @@ def test_verify_graph_replays():
                 torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verify_longest_sequences(sampled):
+    """64 rows, the bound; drafts that mostly stand."""
+    rng = np.random.default_rng(11)
+    ns = [64, 33, 1, 64]
+    cu, logits, draft, ids, ua, us = make(rng, ns, 1500)
+    ids = logits.argmax(1)
+    logits[np.arange(len(ids)), ids] += 20.0
+    draft[np.arange(len(ids)), ids] += 19.0
+    ids[40] = (ids[40] + 1) % 1500
+    out = check(logits, cu, ids, ua * 0.9, us, draft=draft if sampled else None, lens=[70, 40, 9, 64], max_rows=64)
+    # (a sampled draft that neither model finds likely stands or falls with u)
+    assert list(out[0][1:]) == [32, 0, 63] and (sampled or out[0][0] == 40)
+
+
+def test_verify_nothing_to_verify():
+    """No rows at all, and sequences that are all empty."""
+    nv = nvm()
+    for rows in (0, 3):
+        logits = torch.zeros((rows, 50), device="cuda")
+        tokens = torch.full((rows,), 9, dtype=torch.int32, device="cuda")
+        out = nv.Verified(i32([7, 7]), tokens, i32([7, 7]), i32([7, 7]))
+        nv.verify_drafts(logits, i32([0, 0, 0]), i32(np.zeros(rows)), f32(np.zeros(rows)), f32([0.5, 0.5]), 4, kv_lens=i32([3, 0]), out=out)
+        assert out.accepted.tolist() == [0, 0] and out.next.tolist() == [-1, -1] and out.kv_lens.tolist() == [3, 0]
+        assert bool((tokens == 9).all())
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verify_two_streams_at_once_and_replays_of_large_batches(sampled):
+    """Two calls on two streams with workspaces of their own, and a captured one
+    replayed between eager ones."""
+    nv = nvm()
+    sets = [make(np.random.default_rng(s), [3] * 70, 20011) for s in (12, 13)]
+    streams, calls, wants = [torch.cuda.Stream() for _ in sets], [], []
+    for cu, logits, draft, ids, ua, us in sets:
+        args = (f32(logits), i32(cu), i32(ids), f32(ua * 0.5), f32(us), 3)
+        kw = dict(draft_logits=f32(draft) if sampled else None, kv_lens=i32(np.full(70, 40)),
+                  workspace=nv.verify_workspace(3, 70, 20011, "cuda", sampled=sampled))
+        wants.append([t.clone() for t in nv.verify_drafts(*args, **kw)])
+        out = nv.Verified(*(torch.zeros_like(t) for t in wants[-1]))
+        calls.append(lambda args=args, kw=kw, out=out: nv.verify_drafts(*args, out=out, **kw))
+    assert not torch.equal(wants[0][1], wants[1][1])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        outs = []
+        for st, call in zip(streams, calls):
+            with torch.cuda.stream(st):
+                outs.append(call())
+    torch.cuda.synchronize()
+    for out, want in zip(outs, wants):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(streams[0]):
+        with torch.cuda.graph(g, stream=streams[0]):
+            calls[0]()
+    for _ in range(3):
+        for t in outs[0]:
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], wants[0]))
+        calls[1]()
+        torch.cuda.synchronize()
+
+
 def test_rounds_of_speculation():
     """Rounds as they are used: the target's rows (last token and drafts) go
     through q|k|v, the fused rotation and append, attention and o; the logits'
