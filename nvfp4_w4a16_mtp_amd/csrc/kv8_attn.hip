@@ -453,8 +453,8 @@ __global__ __launch_bounds__(256, D == 128 && RT == 1 ? 4 : groups_per_cu(D, RT)
             for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             // Half a chunk at a time: the next half's Q reads and conversions run beside
             // the products of this one (two prompt chunks 400 us with a chunk's reads and
-            // conversions before its products, 364 so; one row each of 32 sequences 100.7
-            // and 97.0).
+            // conversions before its products, 364 so, both with one instruction less a
+            // weight than now; one row each of 32 sequences 100.7 and 97.0).
             bf16x8 kc[2][2], qq[2][RT];
             auto half = [&](int i, bf16x8 (&k)[2]) {
 #pragma unroll
