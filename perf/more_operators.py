@@ -368,7 +368,7 @@ def _plain_attn(st):
     c = st["case"]
     h, g = c["kv_heads"], c["q_heads"] // c["kv_heads"]
     at, outs = 0, []
-    for n in st["n"]:
+    for n in (x for x in st["n"] if x):
         q = st["q"][at:at + n].float().unflatten(1, (h, g)).permute(1, 2, 0, 3).flatten(1, 2)      # [h][g * n][dk]
         k = st["k"][at:at + n].float().permute(1, 2, 0).contiguous()
         v = st["v"][at:at + n].float().transpose(0, 1).contiguous()
