@@ -639,6 +639,34 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
                   size_t ws_bytes, void *stream);
 
 /*
+ * prompt_attention -- causal attention over whole prompts, packed one after the
+ * other, on q, k and v as the projections wrote them (bf16, no cache):
+ * out = softmax(scale * q k^T) v, q head h reading k and v head h / (q_heads /
+ * kv_heads).  Sequence b owns rows [cu_rows[b], cu_rows[b + 1]); its row i sees the
+ * rows j <= i and, with window > 0, of those the last `window` (itself included)
+ * and the first `sinks`.  A prompt that continues a cached one, or single rows over
+ * a cache, are kv8_attention's.
+ *   q, k, v     [rows] head rows (e.g. parts of one q|k|v projection's rows): q's
+ *               heads a multiple of k's and v's, q's dim k's; v may have another.
+ *               Dims: multiples of 8 up to 256.
+ *   cu_rows     device int32 [batch + 1], 4-byte aligned.  Row ranges are cut to
+ *               [0, rows).
+ *   max_rows    host bound of a sequence's rows: those past it are not computed.
+ *   scale, window, sinks     as kv8_attention.
+ *   out         bf16, row r head h at out + r * out_row_stride + h * v.dim,
+ *               16-byte aligned, out_row_stride a multiple of 8, >= q_heads *
+ *               v.dim; must not overlap q, k or v.  Rows outside every sequence
+ *               are left as they were.
+ * Scores, softmax statistics and sums in fp32; weights are rounded to bf16 for the
+ * product with v and for their sum.  What a row does not see never reaches it, NaN
+ * and infinities included.  The result is the same on every call with the same
+ * arguments.  One launch, no workspace.
+ */
+int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const nvfp4_head_rows *v,
+                     const int32_t *cu_rows, int32_t batch, int32_t rows, int32_t max_rows, float scale,
+                     int32_t window, int32_t sinks, uint16_t *out, int64_t out_row_stride, void *stream);
+
+/*
  * verify_drafts -- which drafted tokens stand, and the token after them, from
  * the target's logits and given random numbers (the step after [v4_mtp.rs]
  * `propose`; `after_verify` then trims the cache).  Sequence b owns rows

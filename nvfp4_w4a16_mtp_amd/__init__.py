@@ -27,6 +27,7 @@ Operations (same names as the C ABI):
   rope_kv8_append              ... with q and k rotated in the same launch
   kv8_read                     the cache's values back in bf16
   kv8_attention                attention over that cache (one token to prompt chunks, window and sinks)
+  prompt_attention             attention over whole packed prompts in bf16 (no cache)
   verify_drafts                which drafted tokens stand, the token after them, the cache lengths left
 """
 from __future__ import annotations
@@ -136,6 +137,7 @@ def lib():
         L.verify_drafts_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.verify_drafts_workspace_bytes.restype = sz
         L.verify_drafts.argtypes = [P, i32, i64, i32, P, i64, P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
+        L.prompt_attention.argtypes = [HP, HP, HP, P, i32, i32, i32, f32, i32, i32, P, i64, P]
         L.nvfp4_mtp_last_error.restype = ctypes.c_char_p
         for f in ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_grouped", "w4a16_gemm_m128", "lmhead_gemv_argmax",
                   "lmhead_gemv_argmax_noalloc",
@@ -143,7 +145,8 @@ def lib():
                   "lmhead_gemv_argmax_fc",
                   "w4a16_gemv_embed",
                   "moe_w4a16_gemv", "moe_w4a16_gemv_trace", "moe_layer_w4a16", "moe_workspace_status",
-                  "rope_qk", "kv8_append", "rope_kv8_append", "kv8_read", "kv8_attention", "verify_drafts"):
+                  "rope_qk", "kv8_append", "rope_kv8_append", "kv8_read", "kv8_attention", "verify_drafts",
+                  "prompt_attention"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -937,6 +940,35 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, seqs: KV8Seqs, scale: float 
     _run("kv8_attention", lib().kv8_attention, index, ctypes.byref(dq), cache._ref, seqs._ref(q.shape[0]),
          dq.dim ** -0.5 if scale is None else scale, _fits32(window, "window"), _fits32(sinks, "sinks"), do.data, do.row_stride, workspace.data_ptr(),
          workspace.nbytes)
+    return out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
+                     scale: float | None = None, window: int = 0, sinks: int = 0, out: torch.Tensor | None = None):
+    """Causal attention over packed prompts: q bf16 [rows][q_heads][dim], k
+    [rows][kv_heads][dim], v [rows][kv_heads][dim_v] (rows and heads may be
+    strided); sequence b owns rows cu_rows[b] .. cu_rows[b + 1] (int32 on the
+    device), at most max_rows of them.  scale: dim^-0.5 by default.  out: bf16
+    [rows][q_heads][dim_v], heads contiguous; rows of no sequence are left as
+    they were."""
+    dq, dk, dv, index = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), q.get_device()
+    _int32(cu_rows, "cu_rows")
+    rows = q.shape[0]
+    if cu_rows.dim() != 1 or cu_rows.numel() < 1:
+        raise ValueError("cu_rows must be [batch + 1]")
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError(f"k and v must have q's {rows} rows")
+    shape = (rows, dq.heads, dv.dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    do = _rows(out, "out")
+    if out.shape != shape or do.head_stride != do.dim:
+        raise ValueError(f"out must be {list(shape)} with contiguous heads")
+    _same_device(index, k, v, cu_rows, out)
+    byref = ctypes.byref
+    _run("prompt_attention", lib().prompt_attention, index, byref(dq), byref(dk), byref(dv), cu_rows.data_ptr(),
+         cu_rows.numel() - 1, _fits32(rows, "rows"), _fits32(max_rows, "max_rows"), dq.dim ** -0.5 if scale is None else scale,
+         _fits32(window, "window"), _fits32(sinks, "sinks"), do.data, do.row_stride)
     return out
 
 

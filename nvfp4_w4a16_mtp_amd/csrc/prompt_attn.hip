@@ -1,0 +1,437 @@
+// prompt_attention: causal softmax attention over whole packed prompts
+// (definition in nvfp4_mtp.h).
+#include "kv8.hpp"
+
+namespace nvfp4 {
+
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+constexpr float kPromptSlack = 6.0f;
+
+// Source of the chunks that pad a head to the tile's width.
+__device__ const uint4 kZeroChunk = {0, 0, 0, 0};
+
+struct PromptArgs {
+    HeadRows q, k, v;
+    const int32_t *cu;
+    int batch, rows, max_rows;
+    float scale;            // |scale| * log2(e), 1 for a scale of 0
+    bool negate, zero;      // scale < 0, scale == 0
+    int window, sinks;
+    int heads, group;       // q heads, q heads a kv head
+    int dk, dv;
+    int per_xcd;            // heads / 8, or 0 where 8 does not divide them
+    uint16_t *out;
+    int64_t out_stride;
+};
+
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
+
+// Rows of sequence b, cut to the call's bounds.
+__device__ __forceinline__ int2 prompt_rows(const PromptArgs &a, int b) {
+    const int lo = min(max(a.cu[b], 0), a.rows);
+    const int n = min(max(a.cu[b + 1], lo), a.rows) - lo;
+    return make_int2(lo, min(n, a.max_rows));
+}
+
+// The item-th row tile of R rows: its sequence and its number there, or false.
+// Up to 64 sequences: all sequences' last tiles first, as a tile's keys grow with
+// its number.  More: sequence by sequence, the last tile first.
+template <int R>
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int item, int lane, int &b, int &tile, int2 &sq) {
+    if (a.batch <= 64) {
+        const int2 mine = lane < a.batch ? prompt_rows(a, lane) : make_int2(0, 0);
+        const int nt = (mine.y + R - 1) / R;
+        int lo = -1, hi = (min(a.max_rows, a.rows) + R - 1) / R;    // tiles at or above lo: more than item; above hi: none
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (wave_sum(max(nt - mid, 0)) > item) lo = mid; else hi = mid;
+        }
+        if (lo < 0) return false;
+        tile = lo;
+        const int rank = item - wave_sum(max(nt - lo - 1, 0));
+        uint64_t mask = __ballot(nt > lo);
+        for (int i = 0; i < rank; ++i) mask &= mask - 1;
+        b = __ffsll((unsigned long long)mask) - 1;
+        sq = make_int2(__builtin_amdgcn_readlane(mine.x, b), __builtin_amdgcn_readlane(mine.y, b));
+        return true;
+    }
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        const int2 mine = b0 + lane < a.batch ? prompt_rows(a, b0 + lane) : make_int2(0, 0);
+        const int nt = (mine.y + R - 1) / R;
+        int run = nt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(run, d, 64);
+            if (lane >= d) run += o;
+        }
+        const uint64_t mask = __ballot(before + run > item);
+        if (mask) {
+            const int l = __ffsll((unsigned long long)mask) - 1;
+            b = b0 + l;
+            tile = before + __builtin_amdgcn_readlane(run, l) - 1 - item;
+            sq = make_int2(__builtin_amdgcn_readlane(mine.x, l), __builtin_amdgcn_readlane(mine.y, l));
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(run, 63);
+    }
+    return false;
+}
+
+// Tiles of KT tokens that some row of [lo, hi] sees: those of the sinks, then those
+// from the window's first token on.
+template <int KT>
+struct PromptKeys {
+    int sink_tiles, lo_tile, count;
+    __device__ __forceinline__ PromptKeys(int lo, int hi, int window, int sinks) {
+        lo_tile = window > 0 ? max(lo - window + 1, 0) / KT : 0;
+        const int tiles = hi / KT + 1;
+        sink_tiles = window > 0 ? min((int)(((int64_t)min(sinks, hi + 1) + KT - 1) / KT), lo_tile) : 0;
+        count = sink_tiles + tiles - lo_tile;
+    }
+    __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : lo_tile + i - sink_tiles; }
+};
+
+// 16-byte chunks of a K row in LDS change places by the row's number, so that a read
+// of one chunk of 16 (8) rows meets all banks; 64-byte parts of a V row do, so that a
+// transposing read of one part of four rows does.
+template <int D>
+__device__ __forceinline__ int swizzle_k(int c, int row) { return c ^ (row & (D % 128 ? 7 : 15)); }
+template <int D>
+__device__ __forceinline__ int swizzle_v(int c, int row) { return c ^ ((D % 128 ? (row >> 1) & 1 : row & 3) << 2); }
+
+template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+struct PromptShared {
+    uint16_t k[2][KT][DK];
+    uint16_t v[2][KT][DV];
+};
+
+template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))) void k_prompt(PromptArgs a) {
+    constexpr int R = 32 * NR * WAVES;                // rows a workgroup
+    constexpr int KB = KT / 32, DB = DV / 32;         // 32-token blocks, 32-dim blocks
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    auto &sh = *reinterpret_cast<PromptShared<DK, DV, NR, WAVES, KT, EU> *>(smem);
+    const int wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+
+    int head, item;
+    if (a.per_xcd > 0) {
+        const int j = blockIdx.x >> 3;
+        head = (blockIdx.x & 7) * a.per_xcd + j % a.per_xcd;
+        item = j / a.per_xcd;
+    } else {
+        head = blockIdx.x % a.heads;
+        item = blockIdx.x / a.heads;
+    }
+    int b, tile;
+    int2 sq;
+    if (!find_tile<R>(a, item, lane, b, tile, sq)) return;
+    const int n = scalar(sq.y), r0 = scalar(sq.x), row0 = scalar(tile) * R;
+    const int kvh = head / a.group;
+    const uint16_t *kbase = a.k.data + (int64_t)r0 * a.k.row + (int64_t)kvh * a.k.head;
+    const uint16_t *vbase = a.v.data + (int64_t)r0 * a.v.row + (int64_t)kvh * a.v.head;
+    const PromptKeys<KT> keys(row0, min(row0 + R, n) - 1, a.window, a.sinks);
+
+    // A tile of K and V, straight into LDS: 1 KiB an instruction, the chunk that each
+    // lane loads chosen so that it lands where the swizzle wants it.
+    auto load = [&](int buf, int t0) {
+#pragma unroll
+        for (int i = 0; i < KT * DK / 512 / WAVES; ++i) {
+            const int o = (i * WAVES + wave) * 64 + lane, row = o / (DK / 8), c = swizzle_k<DK>(o % (DK / 8), row);
+            const uint16_t *p = kbase + (int64_t)min(t0 + row, n - 1) * a.k.row + 8 * c;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(8 * c < a.dk ? (const void *)p : &kZeroChunk),
+                                             (__attribute__((address_space(3))) void *)(&sh.k[buf][0][0] + (i * WAVES + wave) * 512), 16, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < KT * DV / 512 / WAVES; ++i) {
+            const int o = (i * WAVES + wave) * 64 + lane, row = o / (DV / 8), c = swizzle_v<DV>(o % (DV / 8), row);
+            const uint16_t *p = vbase + (int64_t)min(t0 + row, n - 1) * a.v.row + 8 * c;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(8 * c < a.dv ? (const void *)p : &kZeroChunk),
+                                             (__attribute__((address_space(3))) void *)(&sh.v[buf][0][0] + (i * WAVES + wave) * 512), 16, 0, 0);
+        }
+    };
+    load(0, keys.tile(0) * KT);
+
+    // the wavefront's rows: column blocks wave and 2 WAVES - 1 - wave of the tile
+    int pos[NR];
+    bf16x8 q[NR][DK / 16];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        pos[r] = row0 + 32 * (r == 0 ? wave : 2 * WAVES - 1 - wave) + col;
+        const uint16_t *p = a.q.data + (int64_t)(r0 + min(pos[r], n - 1)) * a.q.row + (int64_t)head * a.q.head + 8 * half;
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (16 * c + 8 * half < a.dk) w = *reinterpret_cast<const uint4 *>(p + 16 * c);
+            const uint32_t flip = a.negate ? 0x80008000u : 0u;
+            auto prepared = [&](uint32_t x) {
+                if (a.zero) return ((x & 0x7F80u) == 0x7F80u ? x & 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? x & 0xFFFF0000u : 0u);
+                return x ^ flip;
+            };
+            q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(prepared(w.x), prepared(w.y), prepared(w.z), prepared(w.w)));
+        }
+    }
+    auto sees = [&](int t, int p) { return (t <= p) & ((a.window == 0) | (t > p - a.window) | (t < a.sinks)); };
+
+    f32x16 o[NR][DB];
+    float m[NR], l[NR];                               // l: this lane's half of the tokens
+    f32x16 minus_m[NR];
+
+    for (int slow = 0;; ++slow) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m[r] = l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) minus_m[r][i] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
+    }
+    const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
+    for (int it = 0; it < keys.count; ++it) {
+        const int buf = it & 1, t0 = keys.tile(it) * KT;
+        __syncthreads();                              // this tile has arrived, the one before is done with
+        if (it + 1 < keys.count) load(buf ^ 1, keys.tile(it + 1) * KT);
+        const bool part = t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
+        if (slow && part) {                           // V without what is not finite (0 * NaN is NaN)
+            for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
+                uint32_t &w = reinterpret_cast<uint32_t *>(&sh.v[buf][0][0])[i];
+                w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
+            }
+            __syncthreads();
+        }
+        if (t0 > w_hi) continue;                      // (no barrier below)
+        f32x16 s[NR][KB];
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c)
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const int row = 32 * j + col;
+                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(&sh.k[buf][row][8 * swizzle_k<DK>(2 * c + half, row)]);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
+            }
+        const bool whole = t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks);
+        float mx[NR];
+        bool need = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[r][j][i] = sees(t0 + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3), pos[r]) ? s[r][j][i] : -INFINITY;
+            }
+            float x = s[r][0][0];
+#pragma unroll
+            for (int i = 1; i < 16 * KB; ++i) x = fmaxf(x, s[r][i >> 4][i & 15]);
+            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+            mx[r] = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
+            need |= mx[r] * a.scale > kPromptSlack || (l[r] == 0.0f && mx[r] > -INFINITY);
+        }
+        if (__any(need)) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                // (a half may hold no weight yet: the row has one if either does)
+                const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
+                const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
+                const float up = mx[r] == -INFINITY ? 0.0f : fresh ? mx[r] : fmaxf(mx[r], 0.0f);
+                const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
+                m[r] += up;
+                l[r] *= alpha;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
+#pragma unroll
+                for (int j = 0; j < KB; ++j) s[r][j] -= up;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
+            }
+        }
+        bf16x8 p[NR][KB][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        p[r][j][e][i] = static_cast<__bf16>(__builtin_amdgcn_exp2f(s[r][j][8 * e + i] * a.scale));
+                    const uint4 w = __builtin_bit_cast(uint4, p[r][j][e]);
+                    l[r] = dot2(as_bf16x2(w.x), as_bf16x2(0x3F803F80u), l[r]);
+                    l[r] = dot2(as_bf16x2(w.y), as_bf16x2(0x3F803F80u), l[r]);
+                    l[r] = dot2(as_bf16x2(w.z), as_bf16x2(0x3F803F80u), l[r]);
+                    l[r] = dot2(as_bf16x2(w.w), as_bf16x2(0x3F803F80u), l[r]);
+                }
+        // token 32 j + 16 e + 8 (i / 4) + 4 half + i % 4 is element i of the product's
+        // operands: the order in which S comes out
+        auto read_v = [&](int j, int e, int d) {
+            union {
+                s16x4 h[2];
+                bf16x8 v;
+            } u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = 32 * j + 16 * e + 8 * x + 4 * half + ((lane & 15) >> 2);
+                const int c = 4 * d + 2 * (col >> 4) + ((lane & 3) >> 1);
+                u.h[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(
+                    &sh.v[buf][row][8 * swizzle_v<DV>(c, row) + 4 * (lane & 1)]));
+            }
+            return u.v;
+        };
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const bf16x8 vf = read_v(j, e, d);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[r][j][e], o[r][d], 0, 0, 0);
+                }
+        if (slow && part) {
+            // the values left out, to the rows that see them
+#pragma unroll 1
+            for (int t = t0; t < min(t0 + KT, n); ++t) {
+                const uint16_t *vt = vbase + (int64_t)t * a.v.row;
+                bool bad = false;
+                for (int d = lane; d < a.dv; d += 64) bad |= not_finite(vt[d]);
+                if (!__any(bad)) continue;
+#pragma unroll
+                for (int d = 0; d < 4 * DB; ++d) {
+                    const int at = 8 * d + 4 * half;
+                    const uint2 x = *reinterpret_cast<const uint2 *>(vt + (8 * d < a.dv ? at : 0));
+                    const uint32_t w[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (not_finite(w[i]) && sees(t, pos[r])) o[r][d >> 2][4 * (d & 3) + i] += bf16_bits_to_f32(w[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+    if (slow) break;
+    // A value that is not finite may come from a token that its row does not see:
+    // once more, with care.
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) odd |= !(fabsf(o[r][d][i]) <= 3.4028234e38f);
+    if (!__syncthreads_or(odd)) break;
+    load(0, keys.tile(0) * KT);
+    }
+
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
+        const float sum = __uint_as_float(sw.x) + __uint_as_float(sw.y), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (pos[r] >= n) continue;
+        uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int at = 32 * d + 8 * g;
+                if (at >= a.dv) continue;
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = o[r][d][4 * g + i] * inv;
+                *reinterpret_cast<uint2 *>(dst + at) = make_uint2(f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16),
+                                                                  f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16));
+            }
+    }
+}
+
+template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
+    constexpr int R = 32 * NR * WAVES;
+    const size_t lds = sizeof(PromptShared<DK, DV, NR, WAVES, KT, EU>);
+    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, EU>);
+    if (int rc = allow_lds(fn, lds, who)) return rc;
+    // sum over b of ceil(n_b / R)
+    const int64_t most = a.max_rows < a.rows ? a.max_rows : a.rows;
+    int64_t items = (a.rows + (int64_t)a.batch * (R - 1)) / R;
+    const int64_t other = (int64_t)a.batch * ((most + R - 1) / R);
+    if (other < items) items = other;
+    const int64_t blocks = items * a.heads;
+    if (!grid_fits(blocks, 64 * WAVES)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
+    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
+    return check_launch(who);
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const nvfp4_head_rows *v,
+                                const int32_t *cu_rows, int32_t batch, int32_t rows, int32_t max_rows, float scale,
+                                int32_t window, int32_t sinks, uint16_t *out, int64_t out_row_stride, void *stream) {
+    const char *who = "prompt_attention";
+    if (batch < 0 || rows < 0 || max_rows < 0)
+        return fail(NVFP4_ERR_SHAPE, "%s: batch=%d, rows=%d or max_rows=%d < 0", who, batch, rows, max_rows);
+    if (window < 0 || sinks < 0) return fail(NVFP4_ERR_ARG, "%s: window=%d or sinks=%d < 0", who, window, sinks);
+    const float scale2 = __builtin_fabsf(scale) * 1.44269504088896340736f;   // for 2^x
+    if (!__builtin_isfinite(scale2)) return fail(NVFP4_ERR_ARG, "%s: scale * log2(e) is not finite", who);
+    if (batch == 0 || rows == 0 || max_rows == 0) return ok();
+    if (int rc = validate_head_rows(q, who, "q")) return rc;
+    if (int rc = validate_head_rows(k, who, "k")) return rc;
+    if (int rc = validate_head_rows(v, who, "v")) return rc;
+    if (q->heads % k->heads || k->heads != v->heads)
+        return fail(NVFP4_ERR_SHAPE, "%s: %d q heads, %d k heads and %d v heads: k's and v's must be one number that divides q's", who,
+                    q->heads, k->heads, v->heads);
+    if (q->dim != k->dim) return fail(NVFP4_ERR_SHAPE, "%s: q has dim %d, k %d", who, q->dim, k->dim);
+    if (q->dim % 8 || v->dim % 8 || q->dim > 256 || v->dim > 256)
+        return fail(NVFP4_ERR_UNSUPPORTED, "%s: dims %d and %d must be multiples of 8 up to 256", who, q->dim, v->dim);
+    if (!cu_rows || !out) return fail(NVFP4_ERR_ARG, "%s: NULL cu_rows or out", who);
+    if (!aligned(cu_rows, 4) || !aligned(out, 16)) return fail(NVFP4_ERR_ALIGN, "%s: cu_rows not 4-byte or out not 16-byte aligned", who);
+    if (out_row_stride % 8 || out_row_stride < (int64_t)q->heads * v->dim)
+        return fail(NVFP4_ERR_SHAPE, "%s: out_row_stride=%lld must be a multiple of 8 and >= q_heads * v's dim", who,
+                    (long long)out_row_stride);
+    PromptArgs a;
+    a.q = view(q);
+    a.k = view(k);
+    a.v = view(v);
+    a.cu = cu_rows;
+    a.batch = batch;
+    a.rows = rows;
+    a.max_rows = max_rows;
+    // (a hidden token's score of -inf times a scale of 0 would be NaN)
+    a.scale = scale == 0.0f ? 1.0f : scale2;
+    a.negate = scale < 0.0f;
+    a.zero = scale == 0.0f;
+    a.window = window;
+    a.sinks = sinks;
+    a.heads = q->heads;
+    a.group = q->heads / k->heads;
+    a.dk = q->dim;
+    a.dv = v->dim;
+    a.per_xcd = q->heads % 8 ? 0 : q->heads / 8;
+    a.out = out;
+    a.out_stride = out_row_stride;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const int dk = q->dim, dv = v->dim;
+    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2>(a, s, who);
+    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2>(a, s, who);
+    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 1>(a, s, who);
+    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 1>(a, s, who);
+    return launch_prompt<256, 256, 1, 4, 64, 1>(a, s, who);
+}
