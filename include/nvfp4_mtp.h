@@ -545,6 +545,43 @@ typedef struct nvfp4_kv8_seqs {
     int32_t batch, rows, max_rows, max_pages, max_kv_len;
 } nvfp4_kv8_seqs;
 
+/* The pages of a batch of requests over such a cache (host descriptor, device
+ * pointers, 4-byte aligned), kept from step to step by kv8_plan: request b holds the
+ * first held[b] pages of block_table[b]; free_pages[0 .. *free_count) is a stack of the
+ * pages that nobody holds. */
+typedef struct nvfp4_kv8_pool {
+    int32_t *block_table;         /* [batch][max_pages] */
+    int32_t *held;                /* [batch] */
+    int32_t *free_pages;          /* [num_pages] */
+    int32_t *free_count;          /* [1] */
+    int32_t batch, max_pages, num_pages, page_tokens;
+} nvfp4_kv8_pool;
+
+/*
+ * kv8_plan -- the next step's rows and pages from request lengths, on the device
+ * (the lengths that verify_drafts leaves need not come back to the host).  Request b
+ * keeps its first kept_lens[b] tokens and gets new_rows[b] rows after them (0 and 0: it
+ * has ended); a request that is full, max_pages * page_tokens, gets no more, and rows
+ * past `rows` in all are cut.
+ *   cu_rows     out [batch + 1], kv_lens out [batch] (may be kept_lens): with
+ *               pool->block_table the fields of nvfp4_kv8_seqs.
+ *   positions   NULL, or out int32 [rows]: the rows' positions (rope_qk).
+ *   slots       NULL, or out int64 [rows], 8-byte aligned: page * page_tokens +
+ *               position % page_tokens, the row's token in the cache; -1 without a page.
+ *               Rows from cu_rows[batch] on are left as they were.
+ *   missing     out [1]: pages that the pool could not give.
+ * Pages needed are ceil(kv_lens / page_tokens).  First the pages that a request holds
+ * beyond them go back (their table entries become -1), the last request's last page
+ * first; then the missing ones come from the top of the stack, the first request's
+ * first page first, so that a step that is taken back leaves the stack as it was.  Where the
+ * pool is empty the remaining entries become -1 (such tokens are not written and not
+ * attended to), and the next call asks for them again.  Values that make no sense (lengths,
+ * held, free_count below 0 or too large) are cut to their range.  One launch, or two
+ * (many rows).
+ */
+int kv8_plan(const nvfp4_kv8_pool *pool, const int32_t *kept_lens, const int32_t *new_rows, int32_t rows,
+             int32_t *cu_rows, int32_t *kv_lens, int32_t *positions, int64_t *slots, int32_t *missing, void *stream);
+
 /*
  * rope_qk -- rotary positions of q and k rows.
  *   q, q_out    rows before and after (the same shape; q_out may be q itself:

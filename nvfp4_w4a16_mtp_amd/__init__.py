@@ -27,6 +27,7 @@ Operations (same names as the C ABI):
   rope_kv8_append              ... with q and k rotated in the same launch
   kv8_read                     the cache's values back in bf16
   kv8_attention                attention over that cache (one token to prompt chunks, window and sinks)
+  kv8_plan                     a step's block tables, positions and slots from request lengths (KV8Pool)
   prompt_attention             attention over whole packed prompts in bf16 (no cache)
   verify_drafts                which drafted tokens stand, the token after them, the cache lengths left
 """
@@ -81,6 +82,12 @@ class _KV8Seqs(ctypes.Structure):
     _fields_ = [("cu_rows", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
+
+
+class _KV8Pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
 
 
 class NVFP4Error(RuntimeError):
@@ -138,6 +145,7 @@ def lib():
         L.verify_drafts_workspace_bytes.restype = sz
         L.verify_drafts.argtypes = [P, i32, i64, i32, P, i64, P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
         L.prompt_attention.argtypes = [HP, HP, HP, P, i32, i32, i32, f32, i32, i32, P, i64, P]
+        L.kv8_plan.argtypes = [ctypes.POINTER(_KV8Pool), P, P, i32, P, P, P, P, P, P]
         L.nvfp4_mtp_last_error.restype = ctypes.c_char_p
         for f in ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_grouped", "w4a16_gemm_m128", "lmhead_gemv_argmax",
                   "lmhead_gemv_argmax_noalloc",
@@ -146,7 +154,7 @@ def lib():
                   "w4a16_gemv_embed",
                   "moe_w4a16_gemv", "moe_w4a16_gemv_trace", "moe_layer_w4a16", "moe_workspace_status",
                   "rope_qk", "kv8_append", "rope_kv8_append", "kv8_read", "kv8_attention", "verify_drafts",
-                  "prompt_attention"):
+                  "prompt_attention", "kv8_plan"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -778,6 +786,75 @@ class KV8Seqs:
                 self._refs.clear()
             ref = self._refs[rows] = ctypes.byref(d)
         return ref
+
+
+@dataclass(frozen=True)
+class KV8Pool:
+    """The pages of a batch of requests: block_table [batch, max_pages], held
+    [batch] (pages a request holds), free_pages [num_pages] with the count of
+    free ones in free_count [1], a stack.  All int32 on the device, kept by
+    kv8_plan from step to step.  The tensors keep their storage."""
+    block_table: torch.Tensor
+    held: torch.Tensor
+    free_pages: torch.Tensor
+    free_count: torch.Tensor
+    page_tokens: int
+
+    def __post_init__(self):
+        for t, name in ((self.block_table, "block_table"), (self.held, "held"), (self.free_pages, "free_pages"),
+                        (self.free_count, "free_count")):
+            _int32(t, name)
+        batch = self.held.numel()
+        if self.block_table.dim() != 2 or self.block_table.shape[0] != batch or self.free_count.numel() != 1:
+            raise ValueError("need block_table [batch][max_pages], held [batch], free_pages [num_pages], free_count [1]")
+        index = self.held.get_device()
+        _same_device(index, self.block_table, self.free_pages, self.free_count)
+        d = _KV8Pool(self.block_table.data_ptr(), self.held.data_ptr(), self.free_pages.data_ptr(), self.free_count.data_ptr(),
+                     batch, _fits32(self.block_table.shape[1], "max_pages"), _fits32(self.free_pages.numel(), "num_pages"),
+                     _fits32(self.page_tokens, "page_tokens"))
+        for name, v in (("index", index), ("batch", batch), ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, v)
+
+    @staticmethod
+    def empty(num_pages: int, batch: int, max_pages: int, page_tokens: int = 16, device="cuda") -> "KV8Pool":
+        """All pages free, page 0 on top."""
+        def i32(*shape, fill):
+            return torch.full(shape, fill, dtype=torch.int32, device=device)
+        return KV8Pool(i32(batch, max_pages, fill=-1), i32(batch, fill=0),
+                       torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device), i32(1, fill=num_pages), page_tokens)
+
+
+class KV8Plan(NamedTuple):
+    """cu_rows [batch + 1] and kv_lens [batch]: with the pool's block_table the
+    fields of KV8Seqs; positions int32 and slots int64 [rows] (slot: page *
+    page_tokens + position % page_tokens, -1 without a page; rows from
+    cu_rows[batch] on are not written); missing [1]: pages that the pool could
+    not give."""
+    cu_rows: torch.Tensor
+    kv_lens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    missing: torch.Tensor
+
+
+def kv8_plan(pool: KV8Pool, kept_lens: torch.Tensor, new_rows: torch.Tensor, rows: int, out: KV8Plan | None = None) -> KV8Plan:
+    """The next step's rows and pages: request b keeps kept_lens[b] tokens and
+    gets new_rows[b] rows after them (int32 on the device; 0 and 0: it has
+    ended); `rows` bounds all new rows.  Pages no longer needed go back to the
+    pool, missing ones come from it."""
+    index, batch, i32 = pool.index, pool.batch, torch.int32
+    _fits32(rows, "rows")
+    if out is None:
+        if rows < 0:
+            raise ValueError(f"rows={rows} < 0")
+        dev = pool.held.device
+        parts = torch.empty(2 * batch + 2 + rows, dtype=i32, device=dev).split_with_sizes([batch + 1, batch, 1, rows])
+        out = KV8Plan(parts[0], parts[1], parts[3], torch.empty(rows, dtype=torch.int64, device=dev), parts[2])
+    _run("kv8_plan", lib().kv8_plan, index, pool._ref, _vector(kept_lens, i32, batch, index, "kept_lens"),
+         _vector(new_rows, i32, batch, index, "new_rows"), rows, _vector(out.cu_rows, i32, batch + 1, index, "out.cu_rows"),
+         _vector(out.kv_lens, i32, batch, index, "out.kv_lens"), _vector(out.positions, i32, rows, index, "out.positions"),
+         _vector(out.slots, torch.int64, rows, index, "out.slots"), _vector(out.missing, i32, 1, index, "out.missing"))
+    return out
 
 
 def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, mscale: float) -> _Rope:
