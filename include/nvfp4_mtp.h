@@ -458,6 +458,84 @@ int moe_layer_w4a16(const uint16_t *x_bf16, int32_t m, const nvfp4_weight *route
                     const uint16_t *shared_gate_w_bf16, float *y, int32_t *topk_ids, float *topk_w,
                     float *router_logits, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- the MoE for whole batches and prompts: tokens sorted by expert ----
+ *
+ * moe_sort -- the routing of moe_w4a16_gemv for any number of tokens, and its (token,
+ * slot) pairs in the order of their experts.  Pair p = t * top_k + j is token t's j-th
+ * expert.  The sorted order: by expert, then by pair number.
+ *   router_logits  [m][num_experts] fp32, or NULL: topk_ids are given (any values;
+ *                  those outside [0, num_experts) are left out of the order), topk_w
+ *                  is not touched.
+ *   num_experts    1..1024; top_k 1..min(num_experts, 16); m * top_k <= 2^28, m >= 0.
+ *   topk_ids       [m][top_k] int32: experts by descending logit, the lower id first
+ *                  among equal logits (-0 equals +0, NaN comes last).
+ *   topk_w         [m][top_k] fp32: softmax over the chosen logits (NaN where the largest
+ *                  of them is infinite, or one is NaN).
+ *   offsets        out [num_experts + 1] int32: expert e's rows are offsets[e] ..
+ *                  offsets[e + 1].
+ *   order          out [m * top_k] int32: the pair at a sorted place (places from
+ *                  offsets[num_experts] on are left as they were).
+ *   place          out [m * top_k] int32: a pair's place, -1 for one left out.
+ *   workspace      moe_sort_workspace_bytes(m, num_experts, top_k), 4-byte aligned;
+ *                  nothing to initialise; one call at a time per workspace.
+ * One or two launches.
+ */
+size_t moe_sort_workspace_bytes(int32_t m, int32_t num_experts, int32_t top_k);
+int moe_sort(const float *router_logits, int32_t m, int32_t num_experts, int32_t top_k, int32_t *topk_ids, float *topk_w,
+             int32_t *offsets, int32_t *order, int32_t *place, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * moe_gather -- tokens' rows to their sorted places: out[place[t][j]] = x[t].
+ *   x          [m][hidden] fp32 or bf16 (x_dtype NVFP4_OUT_F32 or NVFP4_OUT_BF16),
+ *              16-byte aligned; hidden % 8 == 0.
+ *   place      as moe_sort; pairs whose place is outside [0, m * top_k) are passed
+ *              over, here and in the calls below.
+ *   out        [m * top_k][hidden] of x's type, 16-byte aligned; rows of no pair are
+ *              left as they were.
+ * Its gradient is moe_combine without weights.  One launch.
+ */
+int moe_gather(const void *x, int32_t x_dtype, int32_t m, int32_t hidden, int32_t top_k, const int32_t *place, void *out,
+               void *stream);
+
+/*
+ * moe_combine -- sorted rows back to their tokens, with the weights applied:
+ * y[t] = sum over j, in slot order, of topk_w[t][j] * ys[place[t][j]], fp32 sums.
+ *   ys, y      [m * top_k][hidden] and [m][hidden], fp32 or bf16 each, 16-byte aligned;
+ *              hidden % 8 == 0.  A token without rows becomes zero.
+ *   topk_w     [m][top_k] fp32, or NULL: weights of 1.
+ * One launch.
+ */
+int moe_combine(const void *ys, int32_t ys_dtype, int32_t m, int32_t hidden, int32_t top_k, const int32_t *place,
+                const float *topk_w, void *y, int32_t y_dtype, void *stream);
+
+/*
+ * moe_combine_grad -- the gradient of moe_combine (for experts that are still trained
+ * in bf16 or fp32, before nvfp4_quantize): dys[place[t][j]] = topk_w[t][j] * dy[t] and
+ * dw[t][j] = sum over d of ys[place[t][j]][d] * dy[t][d], fp32 sums.
+ *   dy         [m][hidden] of dy_dtype; ys, dys [m * top_k][hidden] of ys_dtype (dys may
+ *              be ys); rows of no pair are left as they were.
+ *   topk_w     as moe_combine; dw [m][top_k] fp32 (0 for a pair left out).
+ * The result is the same on every call.  One launch.
+ */
+int moe_combine_grad(const void *dy, int32_t dy_dtype, const void *ys, int32_t ys_dtype, int32_t m, int32_t hidden, int32_t top_k,
+                     const int32_t *place, const float *topk_w, void *dys, float *dw, void *stream);
+
+/*
+ * moe_w4a16_gemm -- the routed-expert FFN of moe_w4a16_gemv for any number of rows:
+ * moe_sort, the experts' products over the sorted rows (bf16 MFMA over exactly
+ * dequantized weights, fp32 sums), and the weighted sum of moe_combine.
+ *   x_bf16         [m][H] bf16, 16-byte aligned; m >= 0.
+ *   router_logits, top_k, topk_ids, topk_w     as moe_sort.
+ *   y              out [m][H] of y_dtype, 16-byte aligned; must not overlap x.
+ *   workspace      moe_w4a16_gemm_workspace_bytes(m, top_k, e), 256-byte aligned;
+ *                  nothing to initialise; one call at a time per workspace.
+ * a = bf16_rne(silu(g) * u) as in moe_w4a16_gemv.  H, I % 32 == 0.  The result is the
+ * same on every call.  Four or five launches.
+ */
+size_t moe_w4a16_gemm_workspace_bytes(int32_t m, int32_t top_k, const nvfp4_moe_weights *e);
+int moe_w4a16_gemm(const uint16_t *x_bf16, int32_t m, const float *router_logits, int32_t top_k, const nvfp4_moe_weights *e,
+                   void *y, int32_t y_dtype, int32_t *topk_ids, float *topk_w, void *workspace, size_t ws_bytes, void *stream);
+
 /*
  * moe_workspace_status -- reads and clears the sticky status word of a
  * moe_w4a16_gemv / moe_layer_w4a16 workspace.  In the one-launch path the

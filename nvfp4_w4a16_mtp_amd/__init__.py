@@ -22,6 +22,10 @@ Operations (same names as the C ABI):
   moe_w4a16_gemv_trace         ... one token, with per-workgroup phase timestamps
   moe_layer_w4a16              router + routed experts + gated shared expert
   moe_workspace_status         sticky status of a MoE workspace (host query)
+  moe_sort                     routing of any number of tokens, their pairs sorted by expert (MoeOrder)
+  moe_gather, moe_combine      tokens' rows to their sorted places and, weighted, back
+  moe_combine_grad             the gradient of moe_combine
+  moe_w4a16_gemm               the routed expert FFN for any number of rows
   rope_qk                      rotary positions of q and k rows (rope_frequencies makes the table)
   kv8_append                   k and v rows quantised into a paged 8-bit cache (KV8Cache, KV8Seqs)
   rope_kv8_append              ... with q and k rotated in the same launch
@@ -146,6 +150,15 @@ def lib():
         L.verify_drafts.argtypes = [P, i32, i64, i32, P, i64, P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
         L.prompt_attention.argtypes = [HP, HP, HP, P, i32, i32, i32, f32, i32, i32, P, i64, P]
         L.kv8_plan.argtypes = [ctypes.POINTER(_KV8Pool), P, P, i32, P, P, P, P, P, P]
+        L.moe_sort_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_sort_workspace_bytes.restype = sz
+        L.moe_sort.argtypes = [P, i32, i32, i32, P, P, P, P, P, P, sz, P]
+        L.moe_gather.argtypes = [P, i32, i32, i32, i32, P, P, P]
+        L.moe_combine.argtypes = [P, i32, i32, i32, i32, P, P, P, i32, P]
+        L.moe_combine_grad.argtypes = [P, i32, P, i32, i32, i32, i32, P, P, P, P, P]
+        L.moe_w4a16_gemm_workspace_bytes.argtypes = [i32, i32, EP]
+        L.moe_w4a16_gemm_workspace_bytes.restype = sz
+        L.moe_w4a16_gemm.argtypes = [P, i32, P, i32, EP, P, i32, P, P, P, sz, P]
         L.nvfp4_mtp_last_error.restype = ctypes.c_char_p
         for f in ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_grouped", "w4a16_gemm_m128", "lmhead_gemv_argmax",
                   "lmhead_gemv_argmax_noalloc",
@@ -154,7 +167,8 @@ def lib():
                   "w4a16_gemv_embed",
                   "moe_w4a16_gemv", "moe_w4a16_gemv_trace", "moe_layer_w4a16", "moe_workspace_status",
                   "rope_qk", "kv8_append", "rope_kv8_append", "kv8_read", "kv8_attention", "verify_drafts",
-                  "prompt_attention", "kv8_plan"):
+                  "prompt_attention", "kv8_plan", "moe_sort", "moe_gather", "moe_combine", "moe_combine_grad",
+                  "moe_w4a16_gemm"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -657,6 +671,179 @@ def moe_layer_w4a16(x: torch.Tensor, router: NVFP4Weight, top_k: int, experts: N
                                  workspace.numel(), _stream(x)), "moe_layer_w4a16")
     return out, topk_ids, topk_w, router_logits
 
+
+
+class MoeOrder(NamedTuple):
+    """topk_ids, topk_w [m, top_k]: a token's experts and weights; offsets
+    [experts + 1]: expert e's rows are offsets[e] .. offsets[e + 1] of the
+    sorted pairs; order [m * top_k]: the pair (t * top_k + j) at a place; place
+    [m * top_k]: a pair's place (-1 for one left out)."""
+    topk_ids: torch.Tensor
+    topk_w: torch.Tensor | None
+    offsets: torch.Tensor
+    order: torch.Tensor
+    place: torch.Tensor
+
+    @staticmethod
+    def empty(m: int, top_k: int, experts: int, device) -> "MoeOrder":
+        def new(*shape, dtype=torch.int32):
+            return torch.empty(shape, dtype=dtype, device=device)
+        return MoeOrder(new(m, top_k), new(m, top_k, dtype=torch.float32), new(experts + 1), new(m * top_k), new(m * top_k))
+
+
+def moe_sort_workspace(m: int, top_k: int, experts: int, device) -> torch.Tensor:
+    """Workspace for moe_sort (nothing to initialise)."""
+    for v, name in ((m, "m"), (top_k, "top_k"), (experts, "experts")):
+        _fits32(v, name)
+    nbytes = lib().moe_sort_workspace_bytes(m, experts, top_k)
+    if nbytes == 0:
+        raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _matrix(t: torch.Tensor, dtype, shape, index: int, name: str):
+    """The pointer of a contiguous device tensor of one type (or one of two) and shape."""
+    if (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype is not dtype) or tuple(t.shape) != tuple(shape) or \
+            t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on cuda:{index}")
+    return t.data_ptr()
+
+
+def moe_sort(router_logits: torch.Tensor | None, top_k: int | None = None, topk_ids: torch.Tensor | None = None,
+             experts: int | None = None, workspace: torch.Tensor | None = None, out: MoeOrder | None = None) -> MoeOrder:
+    """Routes the tokens of router_logits (fp32 [m][experts]) to their top_k
+    experts and sorts the (token, slot) pairs by expert.  Or, with topk_ids
+    (int32 [m][top_k]) and `experts` instead of logits, sorts those; ids outside
+    [0, experts) are left out, and topk_w is what `out` holds (None without)."""
+    i32, f32 = torch.int32, torch.float32
+    if (router_logits is None) == (topk_ids is None):
+        raise ValueError("moe_sort needs router_logits or topk_ids")
+    src = topk_ids if router_logits is None else router_logits
+    if not src.is_cuda or src.dim() != 2:
+        raise ValueError("router_logits or topk_ids must be a device matrix")
+    index, m = src.get_device(), src.shape[0]
+    if router_logits is None:
+        if experts is None or (top_k is not None and top_k != topk_ids.shape[1]):
+            raise ValueError("moe_sort of topk_ids needs experts, and top_k as their columns or None")
+        top_k = topk_ids.shape[1]
+        _matrix(topk_ids, i32, (m, top_k), index, "topk_ids")
+        if out is not None and out.topk_ids.data_ptr() != topk_ids.data_ptr():
+            raise ValueError("out.topk_ids must be topk_ids")
+    else:
+        if top_k is None or (experts is not None and experts != router_logits.shape[1]):
+            raise ValueError("moe_sort of router_logits needs top_k, and experts as their columns or None")
+        experts = router_logits.shape[1]
+        _matrix(router_logits, f32, (m, experts), index, "router_logits")
+    for v, name in ((m, "m"), (top_k, "top_k"), (experts, "experts")):
+        _fits32(v, name)
+    if workspace is None:
+        workspace = moe_sort_workspace(m, top_k, experts, src.device)
+    _dev(workspace, "workspace")
+    _same_device(index, workspace)
+    if out is None:
+        out = MoeOrder.empty(m, top_k, experts, src.device)
+        if router_logits is None:
+            out = out._replace(topk_ids=topk_ids, topk_w=None)
+    w = None
+    if router_logits is not None:
+        w = _matrix(out.topk_w, f32, (m, top_k), index, "out.topk_w")
+    _run("moe_sort", lib().moe_sort, index, router_logits.data_ptr() if router_logits is not None else None, m, experts, top_k,
+         _matrix(out.topk_ids, i32, (m, top_k), index, "out.topk_ids"), w, _vector(out.offsets, i32, experts + 1, index, "out.offsets"),
+         _vector(out.order, i32, m * top_k, index, "out.order"), _vector(out.place, i32, m * top_k, index, "out.place"),
+         workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _order_rows(t: torch.Tensor, o: MoeOrder, sorted_rows: bool, name: str):
+    """(index, m, top_k, hidden) of tokens' or sorted rows beside an order."""
+    m, top_k = o.topk_ids.shape
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in _ROW_TYPES or t.shape[0] != (m * top_k if sorted_rows else m) or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous bf16 or fp32 [{m * top_k if sorted_rows else m}][hidden] on the device")
+    return t.get_device(), _fits32(m, "m"), top_k, _fits32(t.shape[1], "hidden")
+
+
+def moe_gather(x: torch.Tensor, o: MoeOrder, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Tokens' rows (bf16 or fp32 [m][hidden]) to their sorted places
+    [m * top_k][hidden]; rows of no pair are left as they were.  Its gradient is
+    moe_combine with weighted=False."""
+    index, m, top_k, hidden = _order_rows(x, o, False, "x")
+    if out is None:
+        out = torch.empty((m * top_k, hidden), dtype=x.dtype, device=x.device)
+    _run("moe_gather", lib().moe_gather, index, x.data_ptr(), _out_code(x.dtype), m, hidden, top_k,
+         _vector(o.place, torch.int32, m * top_k, index, "place"), _matrix(out, x.dtype, (m * top_k, hidden), index, "out"))
+    return out
+
+
+def moe_combine(ys: torch.Tensor, o: MoeOrder, weighted: bool = True, out_dtype: torch.dtype | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Sorted rows (bf16 or fp32) back to their tokens, weighted by topk_w (or
+    by 1) and summed in slot order; out is of ys's type unless said otherwise."""
+    index, m, top_k, hidden = _order_rows(ys, o, True, "ys")
+    if out is None:
+        out = torch.empty((m, hidden), dtype=out_dtype or ys.dtype, device=ys.device)
+    elif out_dtype is not None and out.dtype is not out_dtype:
+        raise ValueError("out is not of out_dtype")
+    _run("moe_combine", lib().moe_combine, index, ys.data_ptr(), _out_code(ys.dtype), m, hidden, top_k,
+         _vector(o.place, torch.int32, m * top_k, index, "place"),
+         _matrix(o.topk_w, torch.float32, (m, top_k), index, "topk_w") if weighted else None,
+         _matrix(out, _ROW_TYPES, (m, hidden), index, "out"), _out_code(out.dtype))
+    return out
+
+
+def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, o: MoeOrder, weighted: bool = True, dys: torch.Tensor | None = None,
+                     dw: torch.Tensor | None = None):
+    """(dys, dw) of moe_combine: dys [m * top_k][hidden] of ys's type (rows of no
+    pair are left as they were; it may be ys), dw fp32 [m][top_k]."""
+    index, m, top_k, hidden = _order_rows(dy, o, False, "dy")
+    if dys is None:
+        dys = torch.empty((m * top_k, hidden), dtype=ys.dtype, device=dy.device)
+    if dw is None:
+        dw = torch.empty((m, top_k), dtype=torch.float32, device=dy.device)
+    _run("moe_combine_grad", lib().moe_combine_grad, index, dy.data_ptr(), _out_code(dy.dtype),
+         _matrix(ys, _ROW_TYPES, (m * top_k, hidden), index, "ys"), _out_code(ys.dtype), m, hidden, top_k,
+         _vector(o.place, torch.int32, m * top_k, index, "place"),
+         _matrix(o.topk_w, torch.float32, (m, top_k), index, "topk_w") if weighted else None,
+         _matrix(dys, ys.dtype, (m * top_k, hidden), index, "dys"), _matrix(dw, torch.float32, (m, top_k), index, "dw"))
+    return dys, dw
+
+
+def moe_gemm_workspace(m: int, top_k: int, experts: NVFP4Experts, device) -> torch.Tensor:
+    """Workspace for moe_w4a16_gemm (nothing to initialise)."""
+    d = experts.desc()
+    nbytes = lib().moe_w4a16_gemm_workspace_bytes(_fits32(m, "m"), _fits32(top_k, "top_k"), ctypes.byref(d))
+    if nbytes == 0:
+        raise NVFP4Error(lib().nvfp4_mtp_last_error().decode(errors="replace"))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def moe_w4a16_gemm(x: torch.Tensor, router_logits: torch.Tensor, top_k: int, experts: NVFP4Experts,
+                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, out_dtype=torch.float32,
+                   topk_ids: torch.Tensor | None = None, topk_w: torch.Tensor | None = None):
+    """moe_w4a16_gemv for any number of rows: (y, topk_ids, topk_w)."""
+    x = _as_bf16(x)
+    _dev(x, "x")
+    index, m, dev = x.get_device(), x.shape[0], x.device
+    if workspace is None:
+        workspace = moe_gemm_workspace(m, top_k, experts, dev)
+    _dev(workspace, "workspace")
+    if out is None:
+        out = torch.empty((m, experts.hidden), dtype=out_dtype, device=dev)
+    if topk_ids is None:
+        topk_ids = torch.empty((m, top_k), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((m, top_k), dtype=torch.float32, device=dev)
+    _same_device(index, workspace, experts.gate_codes)
+    d = experts.desc()
+    _run("moe_w4a16_gemm", lib().moe_w4a16_gemm, index, _matrix(x, torch.bfloat16, (m, experts.hidden), index, "x"), _fits32(m, "m"),
+         _matrix(router_logits, torch.float32, (m, experts.num_experts), index, "router_logits"), _fits32(top_k, "top_k"),
+         ctypes.byref(d), _matrix(out, _ROW_TYPES, (m, experts.hidden), index, "out"), _out_code(out.dtype),
+         _matrix(topk_ids, torch.int32, (m, top_k), index, "topk_ids"), _matrix(topk_w, torch.float32, (m, top_k), index, "topk_w"),
+         workspace.data_ptr(), workspace.nbytes)
+    return out, topk_ids, topk_w
 
 
 # ---- attention of the draft step over a paged 8-bit cache, and verification
