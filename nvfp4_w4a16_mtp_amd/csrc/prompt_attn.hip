@@ -8,10 +8,8 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
-constexpr float kPromptSlack = 6.0f;
-
-// Source of the chunks that pad a head to the tile's width.
-__device__ const uint4 kZeroChunk = {0, 0, 0, 0};
+// A lane's part of a row's weights in one tile that moves the reference.
+constexpr float kPromptSlack = 64.0f;
 
 struct PromptArgs {
     HeadRows q, k, v;
@@ -111,6 +109,62 @@ __device__ __forceinline__ int swizzle_k(int c, int row) { return c ^ (row & (D 
 template <int D>
 __device__ __forceinline__ int swizzle_v(int c, int row) { return c ^ ((D % 128 ? (row >> 1) & 1 : row & 3) << 2); }
 
+// 16 bytes a lane from `from` + at[lane] to `to` + 16 * lane in LDS (from, to: the same
+// in every lane; lanes that are switched off load nothing).  In assembly, as the
+// compiler would wait for it before any later read of LDS; the caller waits
+// (wait_loads) before the barrier that hands the tile over.  m0 has no other user here.
+__device__ __forceinline__ void load_lds(const void *from, uint32_t at, const void *to) {
+    const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(at), "s"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The loads of a tile of KT rows of D elements by WAVES wavefronts: 64 chunks an
+// instruction, chunk o of the tile's LDS by lane o % 64.  Instruction i + P loads what i
+// does, `rows` rows further on.
+template <int D, int KT, int WAVES, bool V>
+struct TileLoad {
+    static constexpr int CH = D / 8, N = KT * CH / 64 / WAVES, P = D % 128 == 64 && D > 64 ? 3 : !V && D == 256 ? 2 : 1;
+    static constexpr int rows = P * 64 * WAVES / CH;
+    static_assert(N % P == 0 && P * 64 * WAVES % CH == 0 && (V || rows % (D % 128 ? 8 : 16) == 0) && rows % 4 == 0, "the pattern repeats");
+    const uint16_t *base;
+    int64_t stride;
+    uint32_t at[P], row[P];
+    bool in[P];
+    __device__ __forceinline__ TileLoad(const uint16_t *first, int64_t row_stride, int dim, int wave, int lane) : base(first), stride(row_stride) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int o = (i * WAVES + wave) * 64 + lane;
+            row[i] = o / CH;
+            int c = V ? swizzle_v<D>(o % CH, row[i]) : swizzle_k<D>(o % CH, row[i]);
+            in[i] = 8 * c < dim;
+            if (!in[i]) c = 0;
+            at[i] = row[i] * (uint32_t)(2 * row_stride) + 16 * c;
+        }
+    }
+    // V's padding is loaded with its first elements (its columns are dropped), K's is
+    // left as it is (zero).
+    __device__ __forceinline__ void load(uint16_t *tile, int t0, int n, int wave) const {
+        const uint16_t *from = base + t0 * stride;
+        if (t0 + KT <= n) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (V || in[i % P]) load_lds(from + (i / P) * rows * stride, at[i % P], tile + (i * WAVES + wave) * 512);
+        } else {                                      // rows past the end: the last one
+            const uint32_t last = n - 1 - t0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t r = row[i % P] + (i / P) * rows;
+                if (V || in[i % P])
+                    load_lds(from, at[i % P] + (min(r, last) - row[i % P]) * (uint32_t)(2 * stride), tile + (i * WAVES + wave) * 512);
+            }
+        }
+    }
+};
+
 template <int DK, int DV, int NR, int WAVES, int KT, int EU>
 struct PromptShared {
     uint16_t k[2][KT][DK];
@@ -143,24 +197,16 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     const uint16_t *vbase = a.v.data + (int64_t)r0 * a.v.row + (int64_t)kvh * a.v.head;
     const PromptKeys<KT> keys(row0, min(row0 + R, n) - 1, a.window, a.sinks);
 
-    // A tile of K and V, straight into LDS: 1 KiB an instruction, the chunk that each
-    // lane loads chosen so that it lands where the swizzle wants it.
+    const TileLoad<DK, KT, WAVES, false> lk(kbase, a.k.row, a.dk, wave, lane);
+    const TileLoad<DV, KT, WAVES, true> lv(vbase, a.v.row, a.dv, wave, lane);
     auto load = [&](int buf, int t0) {
-#pragma unroll
-        for (int i = 0; i < KT * DK / 512 / WAVES; ++i) {
-            const int o = (i * WAVES + wave) * 64 + lane, row = o / (DK / 8), c = swizzle_k<DK>(o % (DK / 8), row);
-            const uint16_t *p = kbase + (int64_t)min(t0 + row, n - 1) * a.k.row + 8 * c;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(8 * c < a.dk ? (const void *)p : &kZeroChunk),
-                                             (__attribute__((address_space(3))) void *)(&sh.k[buf][0][0] + (i * WAVES + wave) * 512), 16, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < KT * DV / 512 / WAVES; ++i) {
-            const int o = (i * WAVES + wave) * 64 + lane, row = o / (DV / 8), c = swizzle_v<DV>(o % (DV / 8), row);
-            const uint16_t *p = vbase + (int64_t)min(t0 + row, n - 1) * a.v.row + 8 * c;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(8 * c < a.dv ? (const void *)p : &kZeroChunk),
-                                             (__attribute__((address_space(3))) void *)(&sh.v[buf][0][0] + (i * WAVES + wave) * 512), 16, 0, 0);
-        }
+        lk.load(&sh.k[buf][0][0], t0, n, wave);
+        lv.load(&sh.v[buf][0][0], t0, n, wave);
     };
+    if (a.dk < DK) {                                  // K's padding
+        for (int i = threadIdx.x; i < (int)sizeof(sh.k) / 16; i += 64 * WAVES) reinterpret_cast<uint4 *>(&sh.k)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     load(0, keys.tile(0) * KT);
 
     // the wavefront's rows: column blocks wave and 2 WAVES - 1 - wave of the tile
@@ -202,6 +248,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
     for (int it = 0; it < keys.count; ++it) {
         const int buf = it & 1, t0 = keys.tile(it) * KT;
+        wait_loads();
         __syncthreads();                              // this tile has arrived, the one before is done with
         if (it + 1 < keys.count) load(buf ^ 1, keys.tile(it + 1) * KT);
         const bool part = t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
@@ -213,73 +260,37 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             __syncthreads();
         }
         if (t0 > w_hi) continue;                      // (no barrier below)
+        // K fragments kAhead steps before the products that use them
+        constexpr int CS = DK / 16, kAhead = 2;
         f32x16 s[NR][KB];
-#pragma unroll
-        for (int c = 0; c < DK / 16; ++c)
+        bf16x8 kf[kAhead + 1][KB];
+        auto read_k = [&](int c) {
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const int row = 32 * j + col;
-                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(&sh.k[buf][row][8 * swizzle_k<DK>(2 * c + half, row)]);
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
+                kf[c % (kAhead + 1)][j] = *reinterpret_cast<const bf16x8 *>(&sh.k[buf][row][8 * swizzle_k<DK>(2 * c + half, row)]);
             }
-        const bool whole = t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks);
-        float mx[NR];
-        bool need = false;
+        };
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            if (!whole) {
+        for (int c = 0; c < kAhead; ++c) read_k(c);
 #pragma unroll
-                for (int j = 0; j < KB; ++j)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[r][j][i] = sees(t0 + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3), pos[r]) ? s[r][j][i] : -INFINITY;
-            }
-            float x = s[r][0][0];
-#pragma unroll
-            for (int i = 1; i < 16 * KB; ++i) x = fmaxf(x, s[r][i >> 4][i & 15]);
-            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-            mx[r] = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
-            need |= mx[r] * a.scale > kPromptSlack || (l[r] == 0.0f && mx[r] > -INFINITY);
-        }
-        if (__any(need)) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                // (a half may hold no weight yet: the row has one if either does)
-                const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
-                const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
-                const float up = mx[r] == -INFINITY ? 0.0f : fresh ? mx[r] : fmaxf(mx[r], 0.0f);
-                const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
-                m[r] += up;
-                l[r] *= alpha;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
-#pragma unroll
-                for (int j = 0; j < KB; ++j) s[r][j] -= up;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
-            }
-        }
-        bf16x8 p[NR][KB][2];
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
+        for (int c = 0; c < CS; ++c) {
+            if (c + kAhead < CS) read_k(c + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < KB; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        p[r][j][e][i] = static_cast<__bf16>(__builtin_amdgcn_exp2f(s[r][j][8 * e + i] * a.scale));
-                    const uint4 w = __builtin_bit_cast(uint4, p[r][j][e]);
-                    l[r] = dot2(as_bf16x2(w.x), as_bf16x2(0x3F803F80u), l[r]);
-                    l[r] = dot2(as_bf16x2(w.y), as_bf16x2(0x3F803F80u), l[r]);
-                    l[r] = dot2(as_bf16x2(w.z), as_bf16x2(0x3F803F80u), l[r]);
-                    l[r] = dot2(as_bf16x2(w.w), as_bf16x2(0x3F803F80u), l[r]);
-                }
+                for (int r = 0; r < NR; ++r)
+                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         // token 32 j + 16 e + 8 (i / 4) + 4 half + i % 4 is element i of the product's
-        // operands: the order in which S comes out
-        auto read_v = [&](int j, int e, int d) {
+        // operands: the order in which S comes out.  Fragment i: j, e, d = i / DB / 2,
+        // i / DB % 2, i % DB; the first kVAhead are read before the softmax.
+        constexpr int kVAhead = 4;
+        bf16x8 vf[kVAhead + 1];
+        auto read_v = [&](int i) {
+            const int d = i % DB, e = i / DB % 2, j = i / DB / 2;
             union {
                 s16x4 h[2];
                 bf16x8 v;
@@ -291,18 +302,80 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 u.h[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(
                     &sh.v[buf][row][8 * swizzle_v<DV>(c, row) + 4 * (lane & 1)]));
             }
-            return u.v;
+            vf[i % (kVAhead + 1)] = u.v;
         };
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
+        for (int i = 0; i < kVAhead; ++i) read_v(i);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool whole = t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks);
+        bf16x8 p[NR][KB][2];
+        float sum[NR];
+        // weights under the present reference, and this lane's part of their sum as rounded
+        auto weigh = [&](int r) {
+            sum[r] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int j = 0; j < KB; ++j)
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const bf16x8 vf = read_v(j, e, d);
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[r][j][e], o[r][d], 0, 0, 0);
+                    for (int i = 0; i < 8; ++i)
+                        p[r][j][e][i] = static_cast<__bf16>(__builtin_amdgcn_exp2f(s[r][j][8 * e + i] * a.scale));
+                    const uint4 w = __builtin_bit_cast(uint4, p[r][j][e]);
+                    sum[r] = dot2(as_bf16x2(w.x), as_bf16x2(0x3F803F80u), sum[r]);
+                    sum[r] = dot2(as_bf16x2(w.y), as_bf16x2(0x3F803F80u), sum[r]);
+                    sum[r] = dot2(as_bf16x2(w.z), as_bf16x2(0x3F803F80u), sum[r]);
+                    sum[r] = dot2(as_bf16x2(w.w), as_bf16x2(0x3F803F80u), sum[r]);
                 }
+        };
+        bool need = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[r][j][i] = sees(t0 + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3), pos[r]) ? s[r][j][i] : -INFINITY;
+            }
+            weigh(r);
+            need |= !(sum[r] <= kPromptSlack) || l[r] == 0.0f;
+        }
+        if (__any(need)) {
+            // move the reference to the present maximum
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float x = s[r][0][0];
+#pragma unroll
+                for (int i = 1; i < 16 * KB; ++i) x = fmaxf(x, s[r][i >> 4][i & 15]);
+                u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+                const float mx = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
+                // (a half may hold no weight yet: the row has one if either does)
+                sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
+                const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
+                const float up = mx == -INFINITY ? 0.0f : fresh ? mx : fmaxf(mx, 0.0f);
+                const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
+                m[r] += up;
+                l[r] *= alpha;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
+#pragma unroll
+                for (int j = 0; j < KB; ++j) s[r][j] -= up;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
+                weigh(r);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) l[r] += sum[r];
+#pragma unroll
+        for (int i = 0; i < 2 * KB * DB; ++i) {
+            if (i + kVAhead < 2 * KB * DB) read_v(i + kVAhead);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                o[r][i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[r][i / DB / 2][i / DB % 2], o[r][i % DB], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (slow && part) {
             // the values left out, to the rows that see them
 #pragma unroll 1
@@ -401,6 +474,9 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     if (q->dim != k->dim) return fail(NVFP4_ERR_SHAPE, "%s: q has dim %d, k %d", who, q->dim, k->dim);
     if (q->dim % 8 || v->dim % 8 || q->dim > 256 || v->dim > 256)
         return fail(NVFP4_ERR_UNSUPPORTED, "%s: dims %d and %d must be multiples of 8 up to 256", who, q->dim, v->dim);
+    // (a tile's rows are addressed in 32 bits)
+    if (k->row_stride >= (1 << 23) || v->row_stride >= (1 << 23))
+        return fail(NVFP4_ERR_UNSUPPORTED, "%s: row strides of k and v must be below 2^23", who);
     if (!cu_rows || !out) return fail(NVFP4_ERR_ARG, "%s: NULL cu_rows or out", who);
     if (!aligned(cu_rows, 4) || !aligned(out, 16)) return fail(NVFP4_ERR_ALIGN, "%s: cu_rows not 4-byte or out not 16-byte aligned", who);
     if (out_row_stride % 8 || out_row_stride < (int64_t)q->heads * v->dim)
