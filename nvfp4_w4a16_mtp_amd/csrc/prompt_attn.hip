@@ -1,5 +1,7 @@
 // prompt_attention: causal softmax attention over whole packed prompts
 // (definition in nvfp4_mtp.h).
+#include <type_traits>
+
 #include "kv8.hpp"
 
 namespace nvfp4 {
@@ -8,8 +10,7 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
-// A lane's part of a row's weights in one tile that moves the reference.
-constexpr float kPromptSlack = 64.0f;
+constexpr float kPromptSlack = 6.0f;
 
 struct PromptArgs {
     HeadRows q, k, v;
@@ -109,18 +110,37 @@ __device__ __forceinline__ int swizzle_k(int c, int row) { return c ^ (row & (D 
 template <int D>
 __device__ __forceinline__ int swizzle_v(int c, int row) { return c ^ ((D % 128 ? (row >> 1) & 1 : row & 3) << 2); }
 
-// 16 bytes a lane from `from` + at[lane] to `to` + 16 * lane in LDS (from, to: the same
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+// The value, unknown to the compiler: what is made from it in a loop stays there
+// (hoisted, the addresses of a tile's reads take more registers than there are).
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// 16 bytes a lane from `from` + at[lane] to LDS address `to` + 16 * lane (from, to: the same
 // in every lane; lanes that are switched off load nothing).  In assembly, as the
 // compiler would wait for it before any later read of LDS; the caller waits
 // (wait_loads) before the barrier that hands the tile over.  m0 has no other user here.
-__device__ __forceinline__ void load_lds(const void *from, uint32_t at, const void *to) {
-    const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)to;
+__device__ __forceinline__ void load_lds(const void *from, uint32_t at, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(at), "s"(from)
+                 : "s"(to), "v"(at), "s"(from)
                  : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// ... from an address of each lane's own.
+__device__ __forceinline__ void load_lds_wide(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(from) : "memory");
+}
+// Waits until at most N of this wavefront's loads are under way (they end in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Source of the chunks that pad a K row.
+__device__ const uint4 kZeroChunk = {0, 0, 0, 0};
 
 // The loads of a tile of KT rows of D elements by WAVES wavefronts: 64 chunks an
 // instruction, chunk o of the tile's LDS by lane o % 64.  Instruction i + P loads what i
@@ -133,8 +153,9 @@ struct TileLoad {
     const uint16_t *base;
     int64_t stride;
     uint32_t at[P], row[P];
-    bool in[P];
-    __device__ __forceinline__ TileLoad(const uint16_t *first, int64_t row_stride, int dim, int wave, int lane) : base(first), stride(row_stride) {
+    bool in[P], pad;
+    __device__ __forceinline__ TileLoad(const uint16_t *first, int64_t row_stride, int dim, int wave, int lane)
+        : base(first), stride(row_stride), pad(!V && dim < D) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int o = (i * WAVES + wave) * 64 + lane;
@@ -145,38 +166,41 @@ struct TileLoad {
             at[i] = row[i] * (uint32_t)(2 * row_stride) + 16 * c;
         }
     }
-    // V's padding is loaded with its first elements (its columns are dropped), K's is
-    // left as it is (zero).
-    __device__ __forceinline__ void load(uint16_t *tile, int t0, int n, int wave) const {
+    __device__ __forceinline__ bool whole(int t0, int n) const { return t0 + KT <= n && !pad; }
+    // Load i of a whole tile from `from`.
+    __device__ __forceinline__ void one(int i, uint32_t tile, const uint16_t *from, int wave) const {
+        load_lds(from + (i / P) * rows * stride, at[i % P], tile + (i * WAVES + wave) * 1024);
+    }
+    // Always N loads a wavefront.  V's padding is its first elements again (its columns
+    // are dropped), K's is zero.
+    __device__ __forceinline__ void load(uint32_t tile, int t0, int n, int wave) const {
         const uint16_t *from = base + t0 * stride;
-        if (t0 + KT <= n) {
+        if (whole(t0, n)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (V || in[i % P]) load_lds(from + (i / P) * rows * stride, at[i % P], tile + (i * WAVES + wave) * 512);
+            for (int i = 0; i < N; ++i) one(i, tile, from, wave);
         } else {                                      // rows past the end: the last one
-            const uint32_t last = n - 1 - t0;
+            const uint32_t last = opaque(n - 1 - t0);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t r = row[i % P] + (i / P) * rows;
-                if (V || in[i % P])
-                    load_lds(from, at[i % P] + (min(r, last) - row[i % P]) * (uint32_t)(2 * stride), tile + (i * WAVES + wave) * 512);
+                const uint32_t o = at[i % P] + (min(r, last) - row[i % P]) * (uint32_t)(2 * stride);
+                load_lds_wide(in[i % P] || V ? (const void *)((const char *)from + o) : &kZeroChunk, tile + (i * WAVES + wave) * 1024);
             }
         }
     }
 };
 
-template <int DK, int DV, int NR, int WAVES, int KT, int EU>
-struct PromptShared {
-    uint16_t k[2][KT][DK];
-    uint16_t v[2][KT][DV];
-};
+// LDS: ST tiles of K, ST of V.
+template <int DK, int DV, int KT, int ST>
+constexpr int prompt_lds() { return ST * KT * (DK + DV) * 2; }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+template <int DK, int DV, int NR, int WAVES, int KT, int ST, int EU>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))) void k_prompt(PromptArgs a) {
     constexpr int R = 32 * NR * WAVES;                // rows a workgroup
     constexpr int KB = KT / 32, DB = DV / 32;         // 32-token blocks, 32-dim blocks
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-    auto &sh = *reinterpret_cast<PromptShared<DK, DV, NR, WAVES, KT, EU> *>(smem);
+    constexpr int kTile = KT * DK * 2, vTile = KT * DV * 2;     // bytes
+    const uint32_t k_lds = lds_address(smem), v_lds = k_lds + ST * kTile;
     const int wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
 
     int head, item;
@@ -199,15 +223,21 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 
     const TileLoad<DK, KT, WAVES, false> lk(kbase, a.k.row, a.dk, wave, lane);
     const TileLoad<DV, KT, WAVES, true> lv(vbase, a.v.row, a.dv, wave, lane);
-    auto load = [&](int buf, int t0) {
-        lk.load(&sh.k[buf][0][0], t0, n, wave);
-        lv.load(&sh.v[buf][0][0], t0, n, wave);
+    // Tile i of K and of V lies in place i % ST; K runs a tile ahead of V.
+    constexpr int kLoads = lk.N + lv.N;
+    auto load_k = [&](int i) { lk.load(k_lds + (i & (ST - 1)) * kTile, keys.tile(i) * KT, n, wave); };
+    auto load_v = [&](int i) { lv.load(v_lds + (i & (ST - 1)) * vTile, keys.tile(i) * KT, n, wave); };
+    auto load_first = [&] {
+        // (a zero that the compiler does not know: it would make the first tiles' masks
+        // and addresses once and keep them)
+        const int first = scalar((int)opaque(0u));
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            if (first + i < keys.count) load_k(first + i);
+            if (i > 0 && first + i - 1 < keys.count) load_v(first + i - 1);
+        }
     };
-    if (a.dk < DK) {                                  // K's padding
-        for (int i = threadIdx.x; i < (int)sizeof(sh.k) / 16; i += 64 * WAVES) reinterpret_cast<uint4 *>(&sh.k)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
-    load(0, keys.tile(0) * KT);
+    load_first();
 
     // the wavefront's rows: column blocks wave and 2 WAVES - 1 - wave of the tile
     int pos[NR];
@@ -221,14 +251,25 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             uint4 w = make_uint4(0, 0, 0, 0);
             if (16 * c + 8 * half < a.dk) w = *reinterpret_cast<const uint4 *>(p + 16 * c);
             const uint32_t flip = a.negate ? 0x80008000u : 0u;
-            auto prepared = [&](uint32_t x) {
-                if (a.zero) return ((x & 0x7F80u) == 0x7F80u ? x & 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? x & 0xFFFF0000u : 0u);
-                return x ^ flip;
-            };
-            q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(prepared(w.x), prepared(w.y), prepared(w.z), prepared(w.w)));
+            q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip));
+        }
+        if (a.zero) {                                 // (what is not finite stays: NaN)
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c) {
+                uint4 w = __builtin_bit_cast(uint4, q[r][c]);
+                auto only_odd = [](uint32_t x) { return (not_finite(x & 0xFFFFu) ? x & 0xFFFFu : 0u) | (not_finite(x >> 16) ? x & 0xFFFF0000u : 0u); };
+                q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(only_odd(w.x), only_odd(w.y), only_odd(w.z), only_odd(w.w)));
+            }
         }
     }
     auto sees = [&](int t, int p) { return (t <= p) & ((a.window == 0) | (t > p - a.window) | (t < a.sinks)); };
+
+    // The lane's place in a tile of K (row col, chunk half) and of V (row 4 half + lane
+    // % 16 / 4, its 8 bytes of the group's 32): the swizzle makes other chunks and parts an exclusive
+    // or with a constant.
+    const int vrow = 4 * half + ((lane & 15) >> 2);
+    const uint32_t k_at = k_lds + col * (2 * DK) + 16 * swizzle_k<DK>(half, col);
+    const uint32_t v_at = v_lds + vrow * (2 * DV) + 16 * swizzle_v<DV>(2 * (col >> 4) + ((lane & 3) >> 1), vrow) + 8 * (lane & 1);
 
     f32x16 o[NR][DB];
     float m[NR], l[NR];                               // l: this lane's half of the tokens
@@ -246,149 +287,237 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
     }
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
-    for (int it = 0; it < keys.count; ++it) {
-        const int buf = it & 1, t0 = keys.tile(it) * KT;
-        wait_loads();
-        __syncthreads();                              // this tile has arrived, the one before is done with
-        if (it + 1 < keys.count) load(buf ^ 1, keys.tile(it + 1) * KT);
-        const bool part = t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
-        if (slow && part) {                           // V without what is not finite (0 * NaN is NaN)
-            for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
-                uint32_t &w = reinterpret_cast<uint32_t *>(&sh.v[buf][0][0])[i];
-                w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
-            }
-            __syncthreads();
+    // Tile i's scores are computed beside the weights of tile i - 1: the products keep the
+    // matrix cores busy while the exponentials keep the vector units.
+    constexpr int CS = DK / 16, kAhead = EU == 2 ? 1 : 2;          // K fragments kAhead steps before their products
+    constexpr int QD = NR * KB * 4;                   // quads of weights
+    f32x16 s[2][NR][KB];
+    bf16x8 p[NR][KB][2];
+    // four weights under the present reference, and their sum as rounded
+    auto weigh = [&](const f32x16 (&x)[NR][KB], int qd) {
+        const int r = qd / (KB * 4), j = qd / 4 % KB, g = qd % 4;
+        bf16x2 w[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(x[r][j][4 * g + i] * a.scale));
+            p[r][j][g >> 1][4 * (g & 1) + i] = w[i >> 1][i & 1];
         }
-        if (t0 > w_hi) continue;                      // (no barrier below)
-        // K fragments kAhead steps before the products that use them
-        constexpr int CS = DK / 16, kAhead = 2;
-        f32x16 s[NR][KB];
+        l[r] = dot2(w[0], as_bf16x2(0x3F803F80u), l[r]);
+        l[r] = dot2(w[1], as_bf16x2(0x3F803F80u), l[r]);
+    };
+    // scores of a tile into y; where BOTH, with the weights of x, the first reads of V, and, where
+    // LOADS, a tile of K and one of V on their way into LDS
+    constexpr int kVAhead = EU == 2 ? 3 : 4;
+    bf16x8 vf[kVAhead + 1];
+    auto score = [&](auto both, auto loads, int tile, f32x16 (&y)[NR][KB], const f32x16 (&x)[NR][KB], auto read_v) {
+        constexpr bool BOTH = decltype(both)::value, LOADS = decltype(loads)::value;
+        uint32_t k_to = 0, v_to = 0;
+        const uint16_t *k_from = nullptr, *v_from = nullptr;
+        if (LOADS) {
+            k_to = k_lds + ((tile - 1 + ST) & (ST - 1)) * kTile;
+            v_to = v_lds + ((tile - 2 + ST) & (ST - 1)) * vTile;
+            k_from = lk.base + keys.tile(tile - 1 + ST) * KT * lk.stride;
+            v_from = lv.base + keys.tile(tile - 2 + ST) * KT * lv.stride;
+        }
+        const uint32_t at = opaque(k_at + (tile & (ST - 1)) * kTile);
         bf16x8 kf[kAhead + 1][KB];
         auto read_k = [&](int c) {
+            constexpr int W = DK % 128 ? 4 : 8;       // steps whose chunks the swizzle mixes
 #pragma unroll
-            for (int j = 0; j < KB; ++j) {
-                const int row = 32 * j + col;
-                kf[c % (kAhead + 1)][j] = *reinterpret_cast<const bf16x8 *>(&sh.k[buf][row][8 * swizzle_k<DK>(2 * c + half, row)]);
-            }
+            for (int j = 0; j < KB; ++j)
+                kf[c % (kAhead + 1)][j] = *reinterpret_cast<const __attribute__((address_space(3))) bf16x8 *>(
+                    (at ^ ((c % W) << 5)) + (c / W) * (32 * W) + 32 * j * (2 * DK));
         };
 #pragma unroll
         for (int c = 0; c < kAhead; ++c) read_k(c);
 #pragma unroll
         for (int c = 0; c < CS; ++c) {
             if (c + kAhead < CS) read_k(c + kAhead);
+            if (BOTH && c >= CS - 2) {
+#pragma unroll
+                for (int i = 0; i < kVAhead; ++i)
+                    if (i % 2 == c - (CS - 2)) read_v(i);
+            }
             __builtin_amdgcn_sched_barrier(0);
+            if (LOADS) {
+#pragma unroll
+                for (int i = c * kLoads / CS; i < (c + 1) * kLoads / CS; ++i) {
+                    if (i < lk.N) lk.one(i, k_to, k_from, wave);
+                    else lv.one(i - lk.N, v_to, v_from, wave);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < KB; ++j)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
+                    y[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : y[r][j], 0, 0, 0);
+            if (BOTH) {
+                constexpr int kPer = (12 * ((QD + CS - 1) / CS) + KB * NR - 1) / (KB * NR);
+#pragma unroll
+                for (int qd = c * QD / CS; qd < (c + 1) * QD / CS; ++qd) weigh(x, qd);
+#pragma unroll
+                for (int k = 0; k < KB * NR; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, kPer, 0);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    auto mask = [&](f32x16 (&x)[NR][KB], int t0) {
+        if (t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks)) return;
+        const int base = (int)opaque(t0 + 4 * half), window = a.window > 0 ? a.window : 0x7FFFFFFF, sink = a.sinks - base;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int here = pos[r] - base, low = here - window;
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 32 * j + 8 * (i >> 2) + (i & 3);     // the token less base
+                    x[r][j][i] = (t <= here) & ((t > low) | (t < sink)) ? x[r][j][i] : -INFINITY;
+                }
+        }
+    };
+    // whether some row of the workgroup does not see some token of a tile
+    auto part = [&](int t0) {
+        return t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
+    };
+    // Moves the reference to the row's maximum so far where scores exceed it by too much,
+    // or where there is none yet.  mx: the lane's maxima of x.
+    auto refer = [&](f32x16 (&x)[NR][KB], float (&mx)[NR]) {
+        bool need = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx[r]), __float_as_uint(mx[r]), false, false);
+            mx[r] = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
+            need |= mx[r] * a.scale > kPromptSlack || l[r] == 0.0f;
+        }
+        if (!__any(need)) return;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            // (a half may hold no weight yet: the row has one if either does)
+            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
+            const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
+            const float up = mx[r] == -INFINITY ? 0.0f : fresh ? mx[r] : fmaxf(mx[r], 0.0f);
+            const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
+            m[r] += up;
+            l[r] *= alpha;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
+#pragma unroll
+            for (int j = 0; j < KB; ++j) x[r][j] -= up;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
+        }
+    };
+    // One tile: x its scores, y the next one's.
+    auto step = [&](int it, f32x16 (&x)[NR][KB], f32x16 (&y)[NR][KB]) {
+        const int t0 = keys.tile(it) * KT;
+        const bool more = it + 1 < keys.count;
+        const int t1 = more ? keys.tile(it + 1) * KT : 0x7FFFFFFF;
+        // V of this tile and K of the next: those of up to ST - 2 later ones may be on their way
+        const int later = keys.count - it - 2;
+        if (ST >= 4 && later >= 2) wait_loads<2 * kLoads>();
+        else if (ST >= 3 && later >= 1) wait_loads<kLoads>();
+        else wait_loads<0>();
+        __syncthreads();
+        const bool fast = it + ST < keys.count && lk.whole(keys.tile(it + ST) * KT, n) && t1 <= w_hi;
+        if (!fast) {
+            if (it + ST < keys.count) load_k(it + ST);
+            if (it + ST - 1 < keys.count) load_v(it + ST - 1);
+        }
+        if (slow && part(t0)) {                           // V without what is not finite (0 * NaN is NaN)
+            for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
+                uint32_t &w = reinterpret_cast<uint32_t *>(smem + ST * kTile + (it & (ST - 1)) * vTile)[i];
+                w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
+            }
+            __syncthreads();
+        }
+        if (t0 > w_hi) return;                        // (no barrier below; nor does a later tile count)
         // token 32 j + 16 e + 8 (i / 4) + 4 half + i % 4 is element i of the product's
         // operands: the order in which S comes out.  Fragment i: j, e, d = i / DB / 2,
-        // i / DB % 2, i % DB; the first kVAhead are read before the softmax.
-        constexpr int kVAhead = 4;
-        bf16x8 vf[kVAhead + 1];
+        // i / DB % 2, i % DB.
+        const uint32_t vat = opaque(v_at + (it & (ST - 1)) * vTile);
         auto read_v = [&](int i) {
             const int d = i % DB, e = i / DB % 2, j = i / DB / 2;
             union {
                 s16x4 h[2];
                 bf16x8 v;
             } u;
+            constexpr int W = DV % 128 ? 2 : 4;       // parts that the swizzle mixes
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int row = 32 * j + 16 * e + 8 * x + 4 * half + ((lane & 15) >> 2);
-                const int c = 4 * d + 2 * (col >> 4) + ((lane & 3) >> 1);
-                u.h[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(
-                    &sh.v[buf][row][8 * swizzle_v<DV>(c, row) + 4 * (lane & 1)]));
-            }
+            for (int z = 0; z < 2; ++z)
+                u.h[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4 *>(
+                    (vat ^ ((d % W) << 6)) + (d / W) * (64 * W) + (32 * j + 16 * e + 8 * z) * (2 * DV)));
             vf[i % (kVAhead + 1)] = u.v;
         };
+        if (t1 <= w_hi) {
+            if (fast) score(std::true_type{}, std::true_type{}, it + 1, y, x, read_v);
+            else score(std::true_type{}, std::false_type{}, it + 1, y, x, read_v);
+            mask(y, t1);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kVAhead; ++i) read_v(i);
-        __builtin_amdgcn_sched_barrier(0);
-        const bool whole = t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks);
-        bf16x8 p[NR][KB][2];
-        float sum[NR];
-        // weights under the present reference, and this lane's part of their sum as rounded
-        auto weigh = [&](int r) {
-            sum[r] = 0.0f;
+            for (int i = 0; i < kVAhead; ++i) read_v(i);
 #pragma unroll
-            for (int j = 0; j < KB; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        p[r][j][e][i] = static_cast<__bf16>(__builtin_amdgcn_exp2f(s[r][j][8 * e + i] * a.scale));
-                    const uint4 w = __builtin_bit_cast(uint4, p[r][j][e]);
-                    sum[r] = dot2(as_bf16x2(w.x), as_bf16x2(0x3F803F80u), sum[r]);
-                    sum[r] = dot2(as_bf16x2(w.y), as_bf16x2(0x3F803F80u), sum[r]);
-                    sum[r] = dot2(as_bf16x2(w.z), as_bf16x2(0x3F803F80u), sum[r]);
-                    sum[r] = dot2(as_bf16x2(w.w), as_bf16x2(0x3F803F80u), sum[r]);
-                }
-        };
-        bool need = false;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            if (!whole) {
-#pragma unroll
-                for (int j = 0; j < KB; ++j)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[r][j][i] = sees(t0 + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3), pos[r]) ? s[r][j][i] : -INFINITY;
-            }
-            weigh(r);
-            need |= !(sum[r] <= kPromptSlack) || l[r] == 0.0f;
+            for (int qd = 0; qd < QD; ++qd) weigh(x, qd);
         }
-        if (__any(need)) {
-            // move the reference to the present maximum
+        // the next tile's maxima beside the products
+        constexpr int PS = 2 * KB * DB, E = 16 * KB;
+        float mx[NR];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float x = s[r][0][0];
+        for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
 #pragma unroll
-                for (int i = 1; i < 16 * KB; ++i) x = fmaxf(x, s[r][i >> 4][i & 15]);
-                u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-                const float mx = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
-                // (a half may hold no weight yet: the row has one if either does)
-                sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
-                const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
-                const float up = mx == -INFINITY ? 0.0f : fresh ? mx : fmaxf(mx, 0.0f);
-                const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
-                m[r] += up;
-                l[r] *= alpha;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
-#pragma unroll
-                for (int j = 0; j < KB; ++j) s[r][j] -= up;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
-                weigh(r);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < NR; ++r) l[r] += sum[r];
-#pragma unroll
-        for (int i = 0; i < 2 * KB * DB; ++i) {
-            if (i + kVAhead < 2 * KB * DB) read_v(i + kVAhead);
+        for (int i = 0; i < PS; ++i) {
+            if (i + kVAhead < PS) read_v(i + kVAhead);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 o[r][i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[r][i / DB / 2][i / DB % 2], o[r][i % DB], 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int k = i * E / PS; k < (i + 1) * E / PS; ++k) mx[r] = fmaxf(mx[r], y[r][k >> 4][k & 15]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (slow && part) {
-            // the values left out, to the rows that see them
-#pragma unroll 1
+        if (t1 <= w_hi) refer(y, mx);
+    };
+    const int first = scalar((int)opaque(0u));
+    if (ST >= 4 && keys.count > 3) wait_loads<3 * kLoads>();
+    else if (keys.count > 1) wait_loads<kLoads>();
+    else wait_loads<0>();
+    __syncthreads();
+    score(std::false_type{}, std::false_type{}, 0, s[0], s[0], [](int) {});
+    mask(s[0], keys.tile(first) * KT);
+    {
+        float mx[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            mx[r] = s[0][r][0][0];
+#pragma unroll
+            for (int i = 1; i < 16 * KB; ++i) mx[r] = fmaxf(mx[r], s[0][r][i >> 4][i & 15]);
+        }
+        refer(s[0], mx);
+    }
+    for (int it = first; it < keys.count; it += 2) {
+        step(it, s[0], s[1]);
+        if (it + 1 < keys.count) step(it + 1, s[1], s[0]);
+    }
+    if (slow) {
+        // the values that were left out, to the rows that see them
+        for (int it = 0; it < keys.count; ++it) {
+            const int t0 = keys.tile(it) * KT;
+            if (!part(t0)) continue;
             for (int t = t0; t < min(t0 + KT, n); ++t) {
                 const uint16_t *vt = vbase + (int64_t)t * a.v.row;
                 bool bad = false;
-                for (int d = lane; d < a.dv; d += 64) bad |= not_finite(vt[d]);
+                for (int d = (int)opaque(lane); d < a.dv; d += 64) bad |= not_finite(vt[d]);
                 if (!__any(bad)) continue;
+                const uint16_t *vl = vt + opaque(4 * half);
 #pragma unroll
                 for (int d = 0; d < 4 * DB; ++d) {
-                    const int at = 8 * d + 4 * half;
-                    const uint2 x = *reinterpret_cast<const uint2 *>(vt + (8 * d < a.dv ? at : 0));
-                    const uint32_t w[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vl + (8 * d < a.dv ? 8 * d : 0));
+                    const uint32_t w[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -398,8 +527,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 }
             }
         }
+        break;
     }
-    if (slow) break;
     // A value that is not finite may come from a token that its row does not see:
     // once more, with care.
     bool odd = false;
@@ -410,7 +539,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll
             for (int i = 0; i < 16; ++i) odd |= !(fabsf(o[r][d][i]) <= 3.4028234e38f);
     if (!__syncthreads_or(odd)) break;
-    load(0, keys.tile(0) * KT);
+    load_first();
     }
 
 #pragma unroll
@@ -434,11 +563,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     }
 }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+template <int DK, int DV, int NR, int WAVES, int KT, int ST, int EU>
 static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
     constexpr int R = 32 * NR * WAVES;
-    const size_t lds = sizeof(PromptShared<DK, DV, NR, WAVES, KT, EU>);
-    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, EU>);
+    const size_t lds = prompt_lds<DK, DV, KT, ST>();
+    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, ST, EU>);
     if (int rc = allow_lds(fn, lds, who)) return rc;
     // sum over b of ceil(n_b / R)
     const int64_t most = a.max_rows < a.rows ? a.max_rows : a.rows;
@@ -447,7 +576,7 @@ static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
     if (other < items) items = other;
     const int64_t blocks = items * a.heads;
     if (!grid_fits(blocks, 64 * WAVES)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
-    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
+    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, ST, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
     return check_launch(who);
 }
 
@@ -505,9 +634,9 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     a.out_stride = out_row_stride;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int dk = q->dim, dv = v->dim;
-    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2>(a, s, who);
-    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2>(a, s, who);
-    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 1>(a, s, who);
-    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 1>(a, s, who);
-    return launch_prompt<256, 256, 1, 4, 64, 1>(a, s, who);
+    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 4, 2>(a, s, who);
+    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 32, 4, 2>(a, s, who);
+    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2, 1>(a, s, who);
+    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 2, 1>(a, s, who);
+    return launch_prompt<256, 256, 1, 4, 64, 2, 1>(a, s, who);
 }
