@@ -12,6 +12,10 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr float kPromptSlack = 6.0f;
 
+// Exponent of the weights' factor in a second pass: sums of up to 2^31 weights of up to
+// 2^kPromptSlack, times values of up to 2^128, stay below 2^128.
+constexpr float kLow = 40.0f;
+
 struct PromptArgs {
     HeadRows q, k, v;
     const int32_t *cu;
@@ -223,19 +227,20 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 
     const TileLoad<DK, KT, WAVES, false> lk(kbase, a.k.row, a.dk, wave, lane);
     const TileLoad<DV, KT, WAVES, true> lv(vbase, a.v.row, a.dv, wave, lane);
-    // Tile i of K and of V lies in place i % ST; K runs a tile ahead of V.
+    // Tile i lies in place i % ST.
     constexpr int kLoads = lk.N + lv.N;
-    auto load_k = [&](int i) { lk.load(k_lds + (i & (ST - 1)) * kTile, keys.tile(i) * KT, n, wave); };
-    auto load_v = [&](int i) { lv.load(v_lds + (i & (ST - 1)) * vTile, keys.tile(i) * KT, n, wave); };
+    auto load = [&](int i) {
+        const int t0 = keys.tile(i) * KT;
+        lk.load(k_lds + (i & (ST - 1)) * kTile, t0, n, wave);
+        lv.load(v_lds + (i & (ST - 1)) * vTile, t0, n, wave);
+    };
     auto load_first = [&] {
-        // (a zero that the compiler does not know: it would make the first tiles' masks
-        // and addresses once and keep them)
+        // (a zero that the compiler does not know: it would make the first tiles'
+        // addresses once and keep them)
         const int first = scalar((int)opaque(0u));
 #pragma unroll
-        for (int i = 0; i < ST; ++i) {
-            if (first + i < keys.count) load_k(first + i);
-            if (i > 0 && first + i - 1 < keys.count) load_v(first + i - 1);
-        }
+        for (int i = 0; i < ST - 1; ++i)
+            if (first + i < keys.count) load(first + i);
     };
     load_first();
 
@@ -287,39 +292,31 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
     }
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
-    // Tile i's scores are computed beside the weights of tile i - 1: the products keep the
-    // matrix cores busy while the exponentials keep the vector units.
-    constexpr int CS = DK / 16, kAhead = EU == 2 ? 1 : 2;          // K fragments kAhead steps before their products
-    constexpr int QD = NR * KB * 4;                   // quads of weights
-    f32x16 s[2][NR][KB];
-    bf16x8 p[NR][KB][2];
+    constexpr int CS = DK / 16, kAhead = 2, kVAhead = 4;        // fragments read ahead of their products
+    const float bias = slow ? -kLow : 0.0f;
+    f32x16 s[NR][KB];
+    bf16x8 p[NR][KB][2], vf[kVAhead + 1];
     // four weights under the present reference, and their sum as rounded
-    auto weigh = [&](const f32x16 (&x)[NR][KB], int qd) {
-        const int r = qd / (KB * 4), j = qd / 4 % KB, g = qd % 4;
+    auto weigh = [&](int r, int qd) {
+        const int j = qd / 4, g = qd % 4;
         bf16x2 w[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(x[r][j][4 * g + i] * a.scale));
+            w[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j][4 * g + i], a.scale, bias)));
             p[r][j][g >> 1][4 * (g & 1) + i] = w[i >> 1][i & 1];
         }
         l[r] = dot2(w[0], as_bf16x2(0x3F803F80u), l[r]);
         l[r] = dot2(w[1], as_bf16x2(0x3F803F80u), l[r]);
     };
-    // scores of a tile into y; where BOTH, with the weights of x, the first reads of V, and, where
-    // LOADS, a tile of K and one of V on their way into LDS
-    constexpr int kVAhead = EU == 2 ? 3 : 4;
-    bf16x8 vf[kVAhead + 1];
-    auto score = [&](auto both, auto loads, int tile, f32x16 (&y)[NR][KB], const f32x16 (&x)[NR][KB], auto read_v) {
-        constexpr bool BOTH = decltype(both)::value, LOADS = decltype(loads)::value;
-        uint32_t k_to = 0, v_to = 0;
-        const uint16_t *k_from = nullptr, *v_from = nullptr;
-        if (LOADS) {
-            k_to = k_lds + ((tile - 1 + ST) & (ST - 1)) * kTile;
-            v_to = v_lds + ((tile - 2 + ST) & (ST - 1)) * vTile;
-            k_from = lk.base + keys.tile(tile - 1 + ST) * KT * lk.stride;
-            v_from = lv.base + keys.tile(tile - 2 + ST) * KT * lv.stride;
-        }
-        const uint32_t at = opaque(k_at + (tile & (ST - 1)) * kTile);
+    // Scores of tile `it` less the reference, with the first reads of V and, where LOADS,
+    // tile `it` + ST - 1 on its way into LDS between the products.
+    auto score = [&](auto loads, int it, auto read_v) {
+        constexpr bool LOADS = decltype(loads)::value;
+        const int to = (it + ST - 1) & (ST - 1);
+        const uint32_t k_to = k_lds + to * kTile, v_to = v_lds + to * vTile;
+        const int64_t t_to = LOADS ? keys.tile(it + ST - 1) * KT : 0;
+        const uint16_t *k_from = lk.base + t_to * lk.stride, *v_from = lv.base + t_to * lv.stride;
+        const uint32_t at = opaque(k_at + (it & (ST - 1)) * kTile);
         bf16x8 kf[kAhead + 1][KB];
         auto read_k = [&](int c) {
             constexpr int W = DK % 128 ? 4 : 8;       // steps whose chunks the swizzle mixes
@@ -333,7 +330,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll
         for (int c = 0; c < CS; ++c) {
             if (c + kAhead < CS) read_k(c + kAhead);
-            if (BOTH && c >= CS - 2) {
+            if (c >= CS - 2) {
 #pragma unroll
                 for (int i = 0; i < kVAhead; ++i)
                     if (i % 2 == c - (CS - 2)) read_v(i);
@@ -350,21 +347,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             for (int j = 0; j < KB; ++j)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    y[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : y[r][j], 0, 0, 0);
-            if (BOTH) {
-                constexpr int kPer = (12 * ((QD + CS - 1) / CS) + KB * NR - 1) / (KB * NR);
-#pragma unroll
-                for (int qd = c * QD / CS; qd < (c + 1) * QD / CS; ++qd) weigh(x, qd);
-#pragma unroll
-                for (int k = 0; k < KB * NR; ++k) {
-                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x402, kPer, 0);
-                }
-            }
+                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    auto mask = [&](f32x16 (&x)[NR][KB], int t0) {
+    auto mask = [&](int t0) {
         if (t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks)) return;
         const int base = (int)opaque(t0 + 4 * half), window = a.window > 0 ? a.window : 0x7FFFFFFF, sink = a.sinks - base;
 #pragma unroll
@@ -375,7 +362,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int t = 32 * j + 8 * (i >> 2) + (i & 3);     // the token less base
-                    x[r][j][i] = (t <= here) & ((t > low) | (t < sink)) ? x[r][j][i] : -INFINITY;
+                    s[r][j][i] = (t <= here) & ((t > low) | (t < sink)) ? s[r][j][i] : -INFINITY;
                 }
         }
     };
@@ -383,12 +370,16 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     auto part = [&](int t0) {
         return t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
     };
-    // Moves the reference to the row's maximum so far where scores exceed it by too much,
-    // or where there is none yet.  mx: the lane's maxima of x.
-    auto refer = [&](f32x16 (&x)[NR][KB], float (&mx)[NR]) {
+    // Moves the reference to the row's maximum where scores exceed it by too much, or
+    // where there is none yet.
+    auto refer = [&] {
+        float mx[NR];
         bool need = false;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
+            mx[r] = s[r][0][0];
+#pragma unroll
+            for (int i = 1; i < 16 * KB; ++i) mx[r] = fmaxf(mx[r], s[r][i >> 4][i & 15]);
             const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx[r]), __float_as_uint(mx[r]), false, false);
             mx[r] = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
             need |= mx[r] * a.scale > kPromptSlack || l[r] == 0.0f;
@@ -406,35 +397,29 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
 #pragma unroll
-            for (int j = 0; j < KB; ++j) x[r][j] -= up;
+            for (int j = 0; j < KB; ++j) s[r][j] -= up;
 #pragma unroll
             for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
         }
     };
-    // One tile: x its scores, y the next one's.
-    auto step = [&](int it, f32x16 (&x)[NR][KB], f32x16 (&y)[NR][KB]) {
+    for (int it = scalar((int)opaque(0u)); it < keys.count; ++it) {
         const int t0 = keys.tile(it) * KT;
-        const bool more = it + 1 < keys.count;
-        const int t1 = more ? keys.tile(it + 1) * KT : 0x7FFFFFFF;
-        // V of this tile and K of the next: those of up to ST - 2 later ones may be on their way
-        const int later = keys.count - it - 2;
+        // up to ST - 2 later tiles may be on their way
+        const int later = keys.count - it - 1;
         if (ST >= 4 && later >= 2) wait_loads<2 * kLoads>();
-        else if (ST >= 3 && later >= 1) wait_loads<kLoads>();
+        else if (ST >= 4 && later >= 1) wait_loads<kLoads>();
         else wait_loads<0>();
-        __syncthreads();
-        const bool fast = it + ST < keys.count && lk.whole(keys.tile(it + ST) * KT, n) && t1 <= w_hi;
-        if (!fast) {
-            if (it + ST < keys.count) load_k(it + ST);
-            if (it + ST - 1 < keys.count) load_v(it + ST - 1);
-        }
-        if (slow && part(t0)) {                           // V without what is not finite (0 * NaN is NaN)
+        __syncthreads();                              // and every wavefront is done with the tile before
+        const bool next = it + ST - 1 < keys.count, fast = next && t0 <= w_hi && lk.whole(keys.tile(it + ST - 1) * KT, n);
+        if (next && !fast) load(it + ST - 1);
+        if (slow && part(t0)) {                       // V without what is not finite (0 * NaN is NaN)
             for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
                 uint32_t &w = reinterpret_cast<uint32_t *>(smem + ST * kTile + (it & (ST - 1)) * vTile)[i];
                 w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
             }
             __syncthreads();
         }
-        if (t0 > w_hi) return;                        // (no barrier below; nor does a later tile count)
+        if (t0 > w_hi) continue;                      // (no barrier below)
         // token 32 j + 16 e + 8 (i / 4) + 4 half + i % 4 is element i of the product's
         // operands: the order in which S comes out.  Fragment i: j, e, d = i / DB / 2,
         // i / DB % 2, i % DB.
@@ -452,56 +437,31 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                     (vat ^ ((d % W) << 6)) + (d / W) * (64 * W) + (32 * j + 16 * e + 8 * z) * (2 * DV)));
             vf[i % (kVAhead + 1)] = u.v;
         };
-        if (t1 <= w_hi) {
-            if (fast) score(std::true_type{}, std::true_type{}, it + 1, y, x, read_v);
-            else score(std::true_type{}, std::false_type{}, it + 1, y, x, read_v);
-            mask(y, t1);
-        } else {
+        if (fast) score(std::true_type{}, it, read_v);
+        else score(std::false_type{}, it, read_v);
+        mask(t0);
+        refer();
+        // The weights of 16 tokens beside the products of the 16 before: exponentials on the
+        // vector units while the matrix cores are busy.
 #pragma unroll
-            for (int i = 0; i < kVAhead; ++i) read_v(i);
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int qd = 0; qd < QD; ++qd) weigh(x, qd);
-        }
-        // the next tile's maxima beside the products
-        constexpr int PS = 2 * KB * DB, E = 16 * KB;
-        float mx[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
+            for (int qd = 0; qd < 2; ++qd) weigh(r, qd);
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int PS = 2 * KB * DB;
 #pragma unroll
         for (int i = 0; i < PS; ++i) {
             if (i + kVAhead < PS) read_v(i + kVAhead);
             __builtin_amdgcn_sched_barrier(0);
+            const int group = i / DB, d = i % DB;
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-                o[r][i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[r][i / DB / 2][i / DB % 2], o[r][i % DB], 0, 0, 0);
+            for (int r = 0; r < NR; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[r][group / 2][group % 2], o[r][d], 0, 0, 0);
+            if (group + 1 < 2 * KB) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                for (int k = i * E / PS; k < (i + 1) * E / PS; ++k) mx[r] = fmaxf(mx[r], y[r][k >> 4][k & 15]);
+                for (int z = d * 2 * NR / DB; z < (d + 1) * 2 * NR / DB; ++z) weigh(z / 2, 2 * (group + 1) + z % 2);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (t1 <= w_hi) refer(y, mx);
-    };
-    const int first = scalar((int)opaque(0u));
-    if (ST >= 4 && keys.count > 3) wait_loads<3 * kLoads>();
-    else if (keys.count > 1) wait_loads<kLoads>();
-    else wait_loads<0>();
-    __syncthreads();
-    score(std::false_type{}, std::false_type{}, 0, s[0], s[0], [](int) {});
-    mask(s[0], keys.tile(first) * KT);
-    {
-        float mx[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            mx[r] = s[0][r][0][0];
-#pragma unroll
-            for (int i = 1; i < 16 * KB; ++i) mx[r] = fmaxf(mx[r], s[0][r][i >> 4][i & 15]);
-        }
-        refer(s[0], mx);
-    }
-    for (int it = first; it < keys.count; it += 2) {
-        step(it, s[0], s[1]);
-        if (it + 1 < keys.count) step(it + 1, s[1], s[0]);
     }
     if (slow) {
         // the values that were left out, to the rows that see them
@@ -634,8 +594,8 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     a.out_stride = out_row_stride;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int dk = q->dim, dv = v->dim;
-    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 4, 2>(a, s, who);
-    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 32, 4, 2>(a, s, who);
+    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2, 2>(a, s, who);
+    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2, 2>(a, s, who);
     if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2, 1>(a, s, who);
     if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 2, 1>(a, s, who);
     return launch_prompt<256, 256, 1, 4, 64, 2, 1>(a, s, who);
