@@ -292,7 +292,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
     }
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
-    constexpr int CS = DK / 16, kAhead = 2, kVAhead = 4;        // fragments read ahead of their products
+    constexpr int CS = DK / 16, kAhead = EU == 1 ? 4 : 2, kVAhead = EU == 1 ? 8 : 4;        // fragments read ahead of their products
     const float bias = slow ? -kLow : 0.0f;
     f32x16 s[NR][KB];
     bf16x8 p[NR][KB][2], vf[kVAhead + 1];
@@ -596,7 +596,7 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     const int dk = q->dim, dv = v->dim;
     if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2, 2>(a, s, who);
     if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2, 2>(a, s, who);
-    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2, 1>(a, s, who);
+    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2, 2>(a, s, who);
     if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 2, 1>(a, s, who);
     return launch_prompt<256, 256, 1, 4, 64, 2, 1>(a, s, who);
 }
