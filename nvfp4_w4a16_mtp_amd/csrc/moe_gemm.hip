@@ -144,6 +144,133 @@ __global__ __launch_bounds__(256) void k_moe_gemm(MoeGemmArgs a) {
         }
 }
 
+// The same for tiles of few rows, whose time is the weights': 16 MT rows of one expert by
+// 64 columns of gate and up (128 of down), a wavefront's 32 weight rows straight from
+// memory into matrix operands.  A lane holds 32 consecutive codes of one weight row, so
+// that an instruction reads 64 bytes of each of 16 rows and four cover whole lines (with
+// the 64-k steps of k_moe_gemm, 32 bytes at a time, the lines and their scales were
+// fetched three times over: 40 rows' gate and up 104 us).  The products take the k of a
+// 128-k step in the order that follows from that, and x is read from LDS in the same one.
+// The next 512 k of weights are on their way during the products of the present ones.
+constexpr int kRowsK = 512, kRowsPitch = kRowsK * 2 + 16;      // bytes of an LDS row of x
+
+template <int MT, bool GATE_UP>
+__global__ __launch_bounds__(256) void k_moe_rows(MoeGemmArgs a) {
+    constexpr int BM = 16 * MT, XQ = BM * (kRowsK / 8) / 256;   // 16-byte chunks of x a thread
+    __shared__ __attribute__((aligned(16))) uint8_t lds[BM * kRowsPitch];
+    const int th = threadIdx.x, lane = th & 63, wave = th >> 6, col = lane & 15, g = lane >> 4;
+    const int t = blockIdx.x / a.cols, nt = blockIdx.x % a.cols;
+    if (t >= *a.tile_count) return;
+    const MoeTile tile = a.tiles[t];
+    const int e = tile.expert, row0 = tile.row, rows = min(a.offsets[e + 1] - row0, BM);
+    // weight rows of the wavefront's two blocks of 16: gate and up, or two of down
+    const int n0 = nt * (GATE_UP ? 64 : 128) + wave * (GATE_UP ? 16 : 32);
+    const uint8_t *crow[2], *srow[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int n = n0 + (GATE_UP ? 0 : 16 * b) + col, which = GATE_UP ? b : 0;
+        const int64_t at = (int64_t)e * a.n + min(n, a.n - 1);
+        crow[b] = a.codes[which] + at * (a.k >> 1) + 16 * g;
+        srow[b] = a.scales[which] + at * (a.k >> 4) + 2 * g;
+    }
+    // x: chunk th % 64 of the rows th / 64 + 4 q; past the tile's rows zeros
+    const int xch = th & 63;
+    const uint16_t *xp[XQ];
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) {
+        const int r = (th >> 6) + 4 * q;
+        xp[q] = nullptr;
+        if (r < rows) xp[q] = a.x + (int64_t)(GATE_UP ? a.order[row0 + r] / a.top_k : row0 + r) * a.k + 8 * xch;
+    }
+    uint4 xr[XQ], cr[2][4];
+    uint32_t sr[2][4];
+    auto load_x = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < XQ; ++q)
+            xr[q] = xp[q] && k0 + 8 * xch < a.k ? *reinterpret_cast<const uint4 *>(xp[q] + k0) : make_uint4(0, 0, 0, 0);
+    };
+    auto load_w = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = k0 + 128 * i + 32 * g < a.k;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                cr[b][i] = make_uint4(0, 0, 0, 0);
+                sr[b][i] = 0;
+                if (in) {
+                    cr[b][i] = *reinterpret_cast<const uint4 *>(crow[b] + (k0 >> 1) + 64 * i);
+                    sr[b][i] = *reinterpret_cast<const uint16_t *>(srow[b] + (k0 >> 4) + 8 * i);
+                }
+            }
+        }
+    };
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    load_x(0);
+    load_w(0);
+    for (int k0 = 0; k0 < a.k; k0 += kRowsK) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < XQ; ++q) *reinterpret_cast<uint4 *>(lds + ((th >> 6) + 4 * q) * kRowsPitch + 16 * xch) = xr[q];
+        __syncthreads();
+        uint4 c[2][4];
+        uint32_t sc[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                c[b][i] = cr[b][i];
+                sc[b][i] = sr[b][i];
+            }
+        if (k0 + kRowsK < a.k) {
+            load_x(k0 + kRowsK);
+            load_w(k0 + kRowsK);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            typedef __attribute__((ext_vector_type(2))) float f32x2;
+            f32x2 sf[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) sf[b] = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc[b][i], false);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {             // eight codes of the lane's 32
+                bf16x8 w[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t word = u == 0 ? c[b][i].x : u == 1 ? c[b][i].y : u == 2 ? c[b][i].z : c[b][i].w;
+                    const float f = u >= 2 ? sf[b].y : sf[b].x;
+                    w[b] = __builtin_bit_cast(bf16x8, make_uint4(moe_dq2<0>(word, f), moe_dq2<1>(word, f), moe_dq2<2>(word, f), moe_dq2<3>(word, f)));
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const bf16x8 x = *reinterpret_cast<const bf16x8 *>(lds + (16 * m + col) * kRowsPitch + 2 * (128 * i + 32 * g + 8 * u));
+                    acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[0], acc[m][0], 0, 0, 0);
+                    acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[1], acc[m][1], 0, 0, 0);
+                }
+            }
+        }
+    }
+    const float dec0 = a.global[0][e].dec, dec1 = GATE_UP ? a.global[1][e].dec : dec0;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * m + 4 * g + r;
+            if (row >= rows) continue;
+            const int64_t at = (int64_t)(row0 + row) * a.n;
+            if (GATE_UP) {
+                const float gate = acc[m][0][r] * dec0, up = acc[m][1][r] * dec1;
+                if (n0 + col < a.n) static_cast<uint16_t *>(a.y)[at + n0 + col] = (uint16_t)f32_to_bf16_bits(gate / (1.0f + expf(-gate)) * up);
+            } else {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (n0 + 16 * b + col < a.n) static_cast<float *>(a.y)[at + n0 + 16 * b + col] = acc[m][b][r] * dec0;
+            }
+        }
+}
+
 struct MoeGemmLayout {
     size_t hist, offsets, order, place, count, tiles, act, down, bytes;
     int bm;
@@ -179,9 +306,9 @@ static MoeGemmLayout moe_gemm_layout(int m, int top_k, const nvfp4_moe_weights *
 template <bool GATE_UP>
 static void launch_moe_gemm(int bm, int64_t blocks, const MoeGemmArgs &a, hipStream_t s) {
     const dim3 g((unsigned)blocks), b(256);
-    if (bm == 16) hipLaunchKernelGGL((k_moe_gemm<16, GATE_UP>), g, b, 0, s, a);
-    else if (bm == 32) hipLaunchKernelGGL((k_moe_gemm<32, GATE_UP>), g, b, 0, s, a);
-    else if (bm == 64) hipLaunchKernelGGL((k_moe_gemm<64, GATE_UP>), g, b, 0, s, a);
+    if (bm == 16) hipLaunchKernelGGL((k_moe_rows<1, GATE_UP>), g, b, 0, s, a);
+    else if (bm == 32) hipLaunchKernelGGL((k_moe_rows<2, GATE_UP>), g, b, 0, s, a);
+    else if (bm == 64) hipLaunchKernelGGL((k_moe_rows<4, GATE_UP>), g, b, 0, s, a);
     else hipLaunchKernelGGL((k_moe_gemm<128, GATE_UP>), g, b, 0, s, a);
 }
 
