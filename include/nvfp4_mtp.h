@@ -466,7 +466,7 @@ int moe_layer_w4a16(const uint16_t *x_bf16, int32_t m, const nvfp4_weight *route
  *   router_logits  [m][num_experts] fp32, or NULL: topk_ids are given (any values;
  *                  those outside [0, num_experts) are left out of the order), topk_w
  *                  is not touched.
- *   num_experts    1..1024; top_k 1..min(num_experts, 16); m * top_k <= 2^28, m >= 0.
+ *   num_experts    1..1024; top_k 1..min(num_experts, 16); m * top_k <= 2^23, m >= 0.
  *   topk_ids       [m][top_k] int32: experts by descending logit, the lower id first
  *                  among equal logits (-0 equals +0, NaN comes last).
  *   topk_w         [m][top_k] fp32: softmax over the chosen logits (NaN where the largest

@@ -6,6 +6,7 @@
 namespace nvfp4 {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kCountBlocks = 256, kPlaceBlocks = 2;
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
@@ -34,11 +35,25 @@ template <int PER>
 __device__ __forceinline__ void choose(const float *lg, int experts, int top_k, int lane, float &my_v, int &my_i) {
     uint32_t v[PER];
     int id[PER];
+    float f[PER];
+    if (PER % 4 == 0 && experts % 4 == 0 && (reinterpret_cast<uintptr_t>(lg) & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < PER; j += 4) {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (lane * PER + j < experts) x = *reinterpret_cast<const float4 *>(lg + lane * PER + j);
+            f[j] = x.x;
+            f[j + 1 < PER ? j + 1 : 0] = x.y;
+            f[j + 2 < PER ? j + 2 : 0] = x.z;
+            f[j + 3 < PER ? j + 3 : 0] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) f[j] = lane * PER + j < experts ? lg[lane * PER + j] : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int e = lane * PER + j;
-        id[j] = e;
-        v[j] = e < experts ? order_key(lg[e]) : 0u;
+        id[j] = lane * PER + j;
+        v[j] = id[j] < experts ? order_key(f[j]) : 0u;
     }
 #pragma unroll
     for (int r = 0; r < PER; ++r)                     // (odd and even neighbours in turn; equals keep their order)
@@ -117,7 +132,10 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a) {
     __shared__ int hist[kMaxExperts];
     const int t0 = blockIdx.x * a.per_block;
     route_block(a, t0, min(t0 + a.per_block, a.m), hist);
-    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = hist[e];
+    // (counts of two experts a word: 2^23 pairs over kCountBlocks blocks fit 16 bits)
+    const int words = (a.experts + 1) / 2;
+    for (int c = threadIdx.x; c < words; c += kSortThreads)
+        a.hist[(int64_t)blockIdx.x * words + c] = hist[2 * c] | (2 * c + 1 < a.experts ? hist[2 * c + 1] << 16 : 0);
 }
 
 // Exclusive prefix sum over the workgroup's threads.
@@ -196,19 +214,34 @@ __device__ __forceinline__ void place_block(const SortArgs &a, int t0, int t1, i
     }
 }
 
+// A block places the pairs of kPlaceBlocks counting blocks.  The counts of all blocks are
+// summed by all threads, a word (two experts) of every (1024 / words)-th block each.
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a, int blocks) {
-    const int tid = threadIdx.x;
-    int count = 0, before = 0;
-    if (tid < a.experts) {
+    __shared__ int all[kMaxExperts], before[kMaxExperts];
+    const int tid = threadIdx.x, words = (a.experts + 1) / 2, groups = kSortThreads / words;
+    all[tid] = before[tid] = 0;
+    __syncthreads();
+    const int c = tid % words, first = (int)blockIdx.x * kPlaceBlocks;
+    if (tid < groups * words) {
+        int n0 = 0, n1 = 0, b0 = 0, b1 = 0;
 #pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-            const int h = a.hist[(int64_t)b * a.experts + tid];
-            count += h;
-            before += b < (int)blockIdx.x ? h : 0;
+        for (int b = tid / words; b < blocks; b += groups) {
+            const uint32_t h = (uint32_t)a.hist[(int64_t)b * words + c];
+            n0 += h & 0xFFFFu;
+            n1 += h >> 16;
+            b0 += b < first ? h & 0xFFFFu : 0;
+            b1 += b < first ? h >> 16 : 0;
+        }
+        atomicAdd(&all[2 * c], n0);
+        atomicAdd(&before[2 * c], b0);
+        if (2 * c + 1 < a.experts) {
+            atomicAdd(&all[2 * c + 1], n1);
+            atomicAdd(&before[2 * c + 1], b1);
         }
     }
-    const int t0 = blockIdx.x * a.per_block;
-    place_block(a, t0, min(t0 + a.per_block, a.m), count, before, blockIdx.x == 0);
+    __syncthreads();
+    const int64_t t0 = (int64_t)first * a.per_block, t1 = t0 + (int64_t)kPlaceBlocks * a.per_block;
+    place_block(a, (int)t0, (int)min(t1, (int64_t)a.m), all[tid], before[tid], blockIdx.x == 0);
 }
 
 // Few tokens: all of it in one workgroup.
@@ -219,12 +252,18 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_one(SortArgs a) {
 }
 
 constexpr int kOneTokens = 32;                        // tokens sorted by one workgroup
-static int sort_per_block(int m) { return m <= 64 * 256 ? 64 : (m + 255) / 256; }
+
+// A token a wavefront, until that makes more than kCountBlocks blocks, whose counts every
+// placing block reads.
+static int sort_per_block(int m) {
+    const int per = (m + kCountBlocks - 1) / kCountBlocks;
+    return per < kSortWaves ? kSortWaves : per;
+}
 
 size_t moe_sort_hist_bytes(int m, int experts) {
     if (m <= kOneTokens) return 0;
     const int per = sort_per_block(m);
-    return (size_t)((m + per - 1) / per) * experts * sizeof(int32_t);
+    return (size_t)((m + per - 1) / per) * ((experts + 1) / 2) * sizeof(int32_t);
 }
 
 void launch_moe_sort(SortArgs a, hipStream_t s) {
@@ -235,7 +274,7 @@ void launch_moe_sort(SortArgs a, hipStream_t s) {
     a.per_block = sort_per_block(a.m);
     const int blocks = (a.m + a.per_block - 1) / a.per_block;
     hipLaunchKernelGGL(k_sort_count, dim3(blocks), dim3(kSortThreads), 0, s, a);
-    hipLaunchKernelGGL(k_sort_place, dim3(blocks), dim3(kSortThreads), 0, s, a, blocks);
+    hipLaunchKernelGGL(k_sort_place, dim3((blocks + kPlaceBlocks - 1) / kPlaceBlocks), dim3(kSortThreads), 0, s, a, blocks);
 }
 
 // ------------------------------------------------------------- rows out and back
@@ -385,14 +424,14 @@ int check_moe_sizes(int m, int experts, int top_k, const char *who) {
         return fail(NVFP4_ERR_SHAPE, "%s: m=%d (need >= 0) or num_experts=%d (need 1..%d)", who, m, experts, kMaxExperts);
     if (top_k < 1 || top_k > kMaxTopK || top_k > experts)
         return fail(NVFP4_ERR_SHAPE, "%s: top_k=%d (need 1..min(num_experts, %d))", who, top_k, kMaxTopK);
-    if ((int64_t)m * top_k > (1 << 28)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: %d x %d pairs are too many", who, m, top_k);
+    if ((int64_t)m * top_k > (1 << 23)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: %d x %d pairs are too many", who, m, top_k);
     return NVFP4_OK;
 }
 
 static int check_rows(int m, int hidden, int top_k, const char *who) {
     if (m < 0 || hidden < 8 || hidden % 8) return fail(NVFP4_ERR_SHAPE, "%s: m=%d hidden=%d (need hidden a multiple of 8)", who, m, hidden);
     if (top_k < 1 || top_k > kMaxTopK) return fail(NVFP4_ERR_SHAPE, "%s: top_k=%d (need 1..%d)", who, top_k, kMaxTopK);
-    if ((int64_t)m * top_k > (1 << 28)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: %d x %d pairs are too many", who, m, top_k);
+    if ((int64_t)m * top_k > (1 << 23)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: %d x %d pairs are too many", who, m, top_k);
     return NVFP4_OK;
 }
 
