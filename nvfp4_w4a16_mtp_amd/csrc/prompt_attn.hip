@@ -12,7 +12,7 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr float kPromptSlack = 6.0f;
 
-// Exponent of the weights' factor in a second pass: sums of up to 2^31 weights of up to
+// Exponent of the weights' factor in a third pass: sums of up to 2^31 weights of up to
 // 2^kPromptSlack, times values of up to 2^128, stay below 2^128.
 constexpr float kLow = 40.0f;
 
@@ -279,8 +279,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     f32x16 o[NR][DB];
     float m[NR], l[NR];                               // l: this lane's half of the tokens
     f32x16 minus_m[NR];
+    bool done[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) done[r] = pos[r] >= n;
 
-    for (int slow = 0;; ++slow) {
+    for (int pass = 0;; ++pass) {
+    const bool slow = pass > 0;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         m[r] = l[r] = 0.0f;
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     }
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
     constexpr int CS = DK / 16, kAhead = EU == 1 ? 4 : 2, kVAhead = EU == 1 ? 8 : 4;        // fragments read ahead of their products
-    const float bias = slow ? -kLow : 0.0f;
+    const float bias = pass > 1 ? -kLow : 0.0f;
     f32x16 s[NR][KB];
     bf16x8 p[NR][KB][2], vf[kVAhead + 1];
     // four weights under the present reference, and their sum as rounded
@@ -390,7 +394,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             // (a half may hold no weight yet: the row has one if either does)
             const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
             const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
-            const float up = mx[r] == -INFINITY ? 0.0f : fresh ? mx[r] : fmaxf(mx[r], 0.0f);
+            // (a row that needs no move stays as it is, whatever its neighbours do)
+            const float up = mx[r] * a.scale > kPromptSlack || (fresh && mx[r] > -INFINITY) ? mx[r] : 0.0f;
             const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
             m[r] += up;
             l[r] *= alpha;
@@ -463,6 +468,22 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+    // A value that is not finite may come from a token that its row does not see, or from a
+    // sum past fp32's range: such rows once more without the former, in the tiles that some
+    // row sees in part, and if that does not help with smaller weights.  The others are done.
+    bool write[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        float far = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) far = __builtin_fmaf(o[r][d][i], 0.0f, far);
+        const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(far), __float_as_uint(far), false, false);
+        const bool odd = !(__uint_as_float(sw.x) + __uint_as_float(sw.y) == 0.0f);      // (0 * NaN and 0 * inf are NaN)
+        write[r] = !done[r] && (!odd || pass == 2);
+        done[r] |= write[r];
+    }
     if (slow) {
         // the values that were left out, to the rows that see them
         for (int it = 0; it < keys.count; ++it) {
@@ -487,26 +508,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 }
             }
         }
-        break;
     }
-    // A value that is not finite may come from a token that its row does not see:
-    // once more, with care.
-    bool odd = false;
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) odd |= !(fabsf(o[r][d][i]) <= 3.4028234e38f);
-    if (!__syncthreads_or(odd)) break;
-    load_first();
-    }
-
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
         const float sum = __uint_as_float(sw.x) + __uint_as_float(sw.y), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (pos[r] >= n) continue;
+        if (!write[r]) continue;
         uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -520,6 +527,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 *reinterpret_cast<uint2 *>(dst + at) = make_uint2(f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16),
                                                                   f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16));
             }
+    }
+    bool left = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) left |= !done[r];
+    if (!__syncthreads_or(left)) break;
+    load_first();
     }
 }
 
