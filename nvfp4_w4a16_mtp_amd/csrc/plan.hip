@@ -24,28 +24,42 @@ struct PlanArgs {
     int32_t *missing;
 };
 
-// Prefix sum over the workgroup's threads, this thread's value included; total: all.
-__device__ __forceinline__ int64_t scan_group(int64_t v, int64_t *waves, int64_t &total) {
+// Sums that stop at 2^32 - 1 (only states that make no sense come near it).
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Prefix sums of N values a thread over the workgroup: v becomes the sum of the threads
+// before this one, total the sum of all.  The caller's last reads of `waves` lie before
+// a barrier.
+template <int N>
+__device__ __forceinline__ void scan_group(uint32_t (&v)[N], uint32_t (*waves)[N], uint32_t (&total)[N]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockDim.x >> 6;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(v, d, 64);
-        if (lane >= d) v += o;
+    for (int k = 0; k < N; ++k) {
+        uint32_t run = v[k];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_up(run, d, 64);
+            if (lane >= d) run = add_sat(run, o);
+        }
+        if (lane == 63) waves[wave][k] = run;
+        v[k] = __shfl_up(run, 1, 64);
+        if (lane == 0) v[k] = 0;
     }
-    __syncthreads();                                  // the last scan's reads of waves are over
-    if (lane == 63) waves[wave] = v;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int i = 0; i < n; ++i) {
-        if (i < wave) before += waves[i];
-        total += waves[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        uint32_t before = 0;
+        total[k] = 0;
+        for (int i = 0; i < n; ++i) {
+            if (i == wave) before = total[k];
+            total[k] = add_sat(total[k], waves[i][k]);
+        }
+        v[k] = add_sat(before, v[k]);
     }
-    return v + before;
 }
 
 // First i with ends[i] > x (ascending; x < ends[n - 1]).
-__device__ __forceinline__ int owner(const int64_t *ends, int n, int64_t x) {
+__device__ __forceinline__ int owner(const uint32_t *ends, int n, uint32_t x) {
     int lo = -1, hi = n - 1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -65,14 +79,15 @@ __device__ __forceinline__ void write_row(const PlanArgs &a, int b, int kept, in
 }
 
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a, int rows_here) {
-    __shared__ int64_t waves[kPlanThreads / 64], ends[kPlanThreads];
-    __shared__ int32_t from[kPlanThreads];
+    constexpr int W = kPlanThreads / 64;
+    __shared__ uint32_t row_sums[W][1], page_sums[2][W][2], ends[3][kPlanThreads];
+    __shared__ int32_t from[3][kPlanThreads];
     const int tid = threadIdx.x, step = blockDim.x;
     const int cap = (int)min((int64_t)a.max_pages << a.lp, (int64_t)0x7FFFFF00);
     const int64_t count = min(max(*a.free_count, 0), a.num_pages);
     const int chunks = (a.batch + step - 1) / step;
 
-    // this thread's request of the present chunk: pages held and needed
+    // this thread's request of a chunk: pages held and needed
     int h = 0, need = 0;
     auto pages = [&](int c) {
         const int b = c * step + tid;
@@ -82,63 +97,81 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a, int rows_here
             need = (a.lens[b] + (1 << a.lp) - 1) >> a.lp;
         }
     };
-    int64_t rows = 0, given = 0, total;
+    uint32_t before[2], total[2], rows_before[1], rows_total[1];   // pages that go, that come; rows
+    int64_t rows = 0, given = 0;
     if (tid == 0) a.cu[0] = 0;
     for (int c = 0; c < chunks; ++c) {
         const int b = c * step + tid;
         int kept = 0, n = 0;
+        h = need = 0;
         if (b < a.batch) {
             kept = min(max(a.kept[b], 0), cap);
             n = min(max(a.fresh[b], 0), cap - kept);
+            h = min(max(a.held[b], 0), a.max_pages);
         }
-        const int64_t end = rows + scan_group(n, waves, total);
-        rows += total;
-        const int lo = (int)min(end - n, (int64_t)a.rows), hi = (int)min(end, (int64_t)a.rows);
+        rows_before[0] = n;
+        scan_group<1>(rows_before, row_sums, rows_total);
+        const int64_t start = rows + rows_before[0];
+        rows += rows_total[0];
+        const int lo = (int)min(start, (int64_t)a.rows), hi = (int)min(start + n, (int64_t)a.rows), len = kept + hi - lo;
         if (b < a.batch) {
             a.cu[b + 1] = hi;
-            a.lens[b] = kept + hi - lo;               // (may be a.kept itself)
+            a.lens[b] = len;                          // (may be a.kept itself)
+            need = (len + (1 << a.lp) - 1) >> a.lp;
         }
-        pages(c);                                     // (this thread's own store)
-        scan_group(max(h - need, 0), waves, total);
-        given += total;
+        ends[2][tid] = hi;                            // for the rows, where this chunk is the only one
+        from[2][tid] = len;
+        before[0] = max(h - need, 0);
+        before[1] = max(need - h, 0);
+        scan_group<2>(before, page_sums[c & 1], total);
+        given += total[0];
     }
     // the pages that go, the first of them on top of the stack
     const int64_t top = count + given;
     int64_t moved = 0;
-    if (given > 0) {
-        for (int c = 0; c < chunks; ++c) {
-            if (chunks > 1) pages(c);
-            ends[tid] = scan_group(max(h - need, 0), waves, total);   // (its barriers follow the last reads of ends)
-            from[tid] = need;
+    for (int c = 0; c < chunks && given > 0; ++c) {
+        if (chunks > 1) {
             __syncthreads();
-            for (int64_t i = tid; i < total; i += step) {
-                const int o = owner(ends, step, i);
-                int32_t *e = a.table + (int64_t)(c * step + o) * a.max_pages + from[o] + (i - (o ? ends[o - 1] : 0));
-                const int64_t at = top - 1 - moved - i;
-                if (at < a.num_pages) a.free_pages[at] = *e;
-                *e = -1;
-            }
-            moved += total;
+            pages(c);
+            before[0] = max(h - need, 0);
+            before[1] = max(need - h, 0);
+            scan_group<2>(before, page_sums[0], total);
         }
+        ends[0][tid] = add_sat(before[0], max(h - need, 0));
+        from[0][tid] = need;
+        __syncthreads();
+        for (uint32_t i = tid; i < total[0]; i += step) {
+            const int o = owner(ends[0], step, i);
+            int32_t *e = a.table + (int64_t)(c * step + o) * a.max_pages + from[0][o] + (i - (o ? ends[0][o - 1] : 0));
+            const int64_t at = top - 1 - moved - i;
+            if (at < a.num_pages) a.free_pages[at] = *e;
+            *e = -1;
+        }
+        moved += total[0];
     }
     // the pages that come, from the top on
     const int64_t have = min(top, (int64_t)a.num_pages);
     int64_t taken = 0;
     for (int c = 0; c < chunks; ++c) {
         const int b = c * step + tid;
-        if (chunks > 1) pages(c);
-        const int want = max(need - h, 0);
-        const int64_t last = scan_group(want, waves, total);
-        ends[tid] = last;
-        from[tid] = h;
-        if (b < a.batch) a.held[b] = min(need, h) + (int)min(max(have - (taken + last - want), (int64_t)0), (int64_t)want);
-        __syncthreads();
-        for (int64_t i = tid; i < total; i += step) {
-            const int o = owner(ends, step, i);
-            const int64_t at = have - 1 - taken - i;
-            a.table[(int64_t)(c * step + o) * a.max_pages + from[o] + (i - (o ? ends[o - 1] : 0))] = at >= 0 ? a.free_pages[at] : -1;
+        if (chunks > 1) {
+            __syncthreads();
+            pages(c);
+            before[0] = max(h - need, 0);
+            before[1] = max(need - h, 0);
+            scan_group<2>(before, page_sums[0], total);
         }
-        taken += total;
+        const int want = max(need - h, 0);
+        ends[1][tid] = add_sat(before[1], want);
+        from[1][tid] = h;
+        if (b < a.batch) a.held[b] = min(need, h) + (int)min(max(have - (taken + before[1]), (int64_t)0), (int64_t)want);
+        __syncthreads();                              // (and the pages given back are in place)
+        for (uint32_t i = tid; i < total[1]; i += step) {
+            const int o = owner(ends[1], step, i);
+            const int64_t at = have - 1 - taken - i;
+            a.table[(int64_t)(c * step + o) * a.max_pages + from[1][o] + (i - (o ? ends[1][o - 1] : 0))] = at >= 0 ? a.free_pages[at] : -1;
+        }
+        taken += total[1];
     }
     if (tid == 0) {
         *a.free_count = (int)max(have - taken, (int64_t)0);
@@ -148,17 +181,18 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a, int rows_here
     __syncthreads();                                  // (the tables and cu are this workgroup's own stores)
     for (int c = 0; c < chunks; ++c) {
         const int b = c * step + tid, n = min(a.batch - c * step, step);
-        __syncthreads();
-        const int first = a.cu[c * step];
-        if (b < a.batch) {
-            ends[tid] = a.cu[b + 1];
-            from[tid] = a.lens[b];
+        int first = 0;
+        if (chunks > 1) {
+            __syncthreads();
+            first = a.cu[c * step];
+            ends[2][tid] = b < a.batch ? a.cu[b + 1] : 0;
+            from[2][tid] = b < a.batch ? a.lens[b] : 0;
+            __syncthreads();
         }
-        __syncthreads();
-        for (int r = first + tid; r < (int)ends[n - 1]; r += step) {
-            const int o = owner(ends, n, r);
+        for (int r = first + tid; r < (int)ends[2][n - 1]; r += step) {
+            const int o = owner(ends[2], n, r);
             // (the request's last row is its last token)
-            write_row(a, c * step + o, from[o] - (int)ends[o], r, r);
+            write_row(a, c * step + o, from[2][o] - (int)ends[2][o], r, r);
         }
     }
 }
