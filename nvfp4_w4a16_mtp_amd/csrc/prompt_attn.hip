@@ -129,14 +129,16 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
 // compiler would wait for it before any later read of LDS; the caller waits
 // (wait_loads) before the barrier that hands the tile over.  m0 has no other user here.
 __device__ __forceinline__ void load_lds(const void *from, uint32_t at, uint32_t to) {
+    const uint64_t f = reinterpret_cast<uint64_t>(from);
+    const uint64_t base = (uint64_t)(uint32_t)scalar((int)(f >> 32)) << 32 | (uint32_t)scalar((int)f);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(to), "v"(at), "s"(from)
+                 : "s"(scalar((int)to)), "v"(at), "s"(base)
                  : "memory");
 }
 // ... from an address of each lane's own.
 __device__ __forceinline__ void load_lds_wide(const void *from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(scalar((int)to)), "v"(from) : "memory");
 }
 // Waits until at most N of this wavefront's loads are under way (they end in order).
 template <int N>
