@@ -298,7 +298,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
     }
     const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
-    constexpr int CS = DK / 16, kAhead = EU == 1 ? 4 : 2, kVAhead = EU == 1 ? 8 : 4;        // fragments read ahead of their products
+    constexpr int CS = DK / 16, kAhead = EU == 1 ? 3 : 2, kVAhead = EU == 1 ? 5 : 4;        // fragments read ahead of their products
     const float bias = pass > 1 ? -kLow : 0.0f;
     f32x16 s[NR][KB];
     bf16x8 p[NR][KB][2], vf[kVAhead + 1];
