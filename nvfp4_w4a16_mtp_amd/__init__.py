@@ -703,6 +703,8 @@ def moe_sort_workspace(m: int, top_k: int, experts: int, device) -> torch.Tensor
 
 def _matrix(t: torch.Tensor, dtype, shape, index: int, name: str):
     """The pointer of a contiguous device tensor of one type (or one of two) and shape."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype is not dtype) or tuple(t.shape) != tuple(shape) or \
             t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on cuda:{index}")

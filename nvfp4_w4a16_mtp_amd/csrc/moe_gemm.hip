@@ -10,7 +10,7 @@
 
 namespace nvfp4 {
 
-constexpr int kMoeBN = 128, kMoeBK = 64;
+constexpr int kMoeBM = 128, kMoeBN = 128, kMoeBK = 64;
 
 // As the prompt GEMM's: 16-byte chunk c of a 128-byte row r at place c ^ (r % 8).
 __device__ __forceinline__ int moe_off(int r, int c) { return r * 128 + 16 * (c ^ (r & 7)); }
@@ -34,13 +34,18 @@ struct MoeGemmArgs {
     void *y;                      // bf16 [pairs][n] or fp32 [pairs][n]
 };
 
-// One row tile (BM rows of one expert) by 128 weight rows.  GATE_UP: 64 rows of
+// One row tile (128 rows of one expert) by 128 weight rows, dequantized on the way into LDS
+// as in the prompt GEMM, whose 128-row rate it reaches (4096 rows of top-8 of 256 experts:
+// 393 tiles, 65% full, gate and up 268 us, 787 TFLOP/s counting whole tiles).  Measured
+// against it there: 64-row tiles 314 us, 256-row tiles 359, 128-k steps 314, four
+// wavefronts a SIMD 392 (they spill), the weights of four steps asked for at once 294, a row
+// tile's columns on one XCD 268.  GATE_UP: 64 rows of
 // gate and the same 64 of up, in turn by 16, so that a wavefront has both of an output.
-template <int BM, bool GATE_UP>
+template <bool GATE_UP>
 __global__ __launch_bounds__(256) void k_moe_gemm(MoeGemmArgs a) {
-    constexpr int WM = BM >= 128 ? 2 : 1, WN = 4 / WM;          // wavefronts along rows and columns
+    constexpr int BM = kMoeBM, WM = 2, WN = 2;                  // wavefronts along rows and columns
     constexpr int MI = BM / 16 / WM, NJ = kMoeBN / 16 / WN;
-    constexpr int XQ = (BM * 8 + 255) / 256;                    // 16-byte chunks of x a thread
+    constexpr int XQ = BM * 8 / 256;                            // 16-byte chunks of x a thread
     __shared__ __attribute__((aligned(16))) uint8_t lds_a[BM * 128];
     __shared__ __attribute__((aligned(16))) uint8_t lds_b[kMoeBN * 128];
     const int th = threadIdx.x, lane = th & 63, wave = th >> 6;
@@ -95,7 +100,7 @@ __global__ __launch_bounds__(256) void k_moe_gemm(MoeGemmArgs a) {
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < XQ; ++q)
-            if (BM >= 32 || th < BM * 8) *reinterpret_cast<uint4 *>(lds_a + moe_off((th >> 3) + 32 * q, xch)) = xr[q];
+            *reinterpret_cast<uint4 *>(lds_a + moe_off((th >> 3) + 32 * q, xch)) = xr[q];
         typedef __attribute__((ext_vector_type(2))) float f32x2;
         const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8((int)sr, false);
         const uint32_t w[4] = {cr.x, cr.y, cr.z, cr.w};
@@ -282,7 +287,11 @@ static MoeGemmLayout moe_gemm_layout(int m, int top_k, const nvfp4_moe_weights *
     MoeGemmLayout l;
     const int64_t pairs = (int64_t)m * top_k, E = e->num_experts;
     const int64_t avg = pairs / E;
-    l.bm = avg <= 12 ? 16 : avg <= 24 ? 32 : avg <= 48 ? 64 : 128;
+    // Tiles that hold the average expert's rows with some to spare: a tile costs its weights
+    // once however few rows it has, and a row past the last tile another one.  (40 rows of top-8
+    // of 256, 1.25 rows an expert: 16-row tiles of k_moe_rows 57 us for gate and up, of
+    // k_moe_gemm 104; 4096 rows, 128 an expert: 128-row tiles 268, 64-row ones 314.)
+    l.bm = avg <= 12 ? 16 : avg <= 24 ? 32 : avg <= 48 ? 64 : kMoeBM;
     // sum over the experts of ceil(n_e / bm)
     l.max_tiles = pairs / l.bm + (pairs < E ? pairs : E);
     size_t at = 0;
@@ -309,7 +318,7 @@ static void launch_moe_gemm(int bm, int64_t blocks, const MoeGemmArgs &a, hipStr
     if (bm == 16) hipLaunchKernelGGL((k_moe_rows<1, GATE_UP>), g, b, 0, s, a);
     else if (bm == 32) hipLaunchKernelGGL((k_moe_rows<2, GATE_UP>), g, b, 0, s, a);
     else if (bm == 64) hipLaunchKernelGGL((k_moe_rows<4, GATE_UP>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_moe_gemm<128, GATE_UP>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_moe_gemm<GATE_UP>), g, b, 0, s, a);
 }
 
 static int check_experts(const nvfp4_moe_weights *e, const char *who) {

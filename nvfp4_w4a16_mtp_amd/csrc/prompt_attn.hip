@@ -1,5 +1,37 @@
 // prompt_attention: causal softmax attention over whole packed prompts
 // (definition in nvfp4_mtp.h).
+//
+// For each row: o = sum_t p_t v_t / sum_t p_t with p_t = 2^((q.k_t - m) scale'), one pass
+// over the keys with a running reference m and sum (fp32).  Must compute 2 (dk + dv) flop
+// a visible (row, key) pair and query head; the bytes (q, k, v and the result once) are
+// nothing beside that for long prompts.
+//
+// A workgroup of four wavefronts takes 128 rows of one query head, a wavefront 32 of them
+// with all dims of their sums in registers, and walks the keys in tiles of 64 tokens with
+// v_mfma_f32_32x32x16_bf16:
+//   S^T = K Q^T    A = K (32 tokens), B = Q^T (32 rows, in registers throughout);
+//   O^T = V^T P^T  A = V^T (32 dims), B = P^T.
+// A lane's column is a row of queries in both products, and S^T comes out of the first in
+// a lane order that is the second's operand order up to a permutation of the tokens; V is
+// read in the same permutation (transposing LDS reads), so P never leaves its registers.
+// Tiles go from memory straight into LDS (double buffered, swizzled at the source so that no
+// read has a bank conflict: none counted), each fragment is read a few products ahead.
+//  - The first product accumulates onto -m, so a weight is one multiplication and 2^x, and the
+//    reference moves only where a row's score exceeds it by kPromptSlack (2^6 in the weights).
+//  - The weights of 16 tokens are made beside the products of the 16 before: exponentials run
+//    on the vector units while the matrix cores are busy (12001 rows, 16 + 2 heads of 256:
+//    2257 us with no read-ahead, 1552 with it, 1337 so; the next tile's scores beside this
+//    one's weights 1238 us there, but 64 more registers: packed prompts of 128 dims 506 us
+//    against 406).
+//  - 64-token tiles: 32-token ones with four stages spill or pay the barrier twice (128 dims:
+//    506 us).  Two workgroups a CU where the registers allow (dims up to 192 x 128: windowed
+//    prompts 465 -> 388 us); 192 x 192 and 256 x 256 have one wavefront a SIMD.
+//  - 24 prompts of up to 4500 rows, 32 + 8 heads of 128: 415 us, 857 TFLOP/s; 12001 rows of
+//    256 dims: 1337 us, 882 TFLOP/s (an 8192^3 product reaches 1222).  With everything but the
+//    products and barriers left out the latter takes 915 us.  What bounds it: one wavefront a
+//    SIMD with little to cover the waits between its two products.
+// Long prompts' tiles first: the keys of a row tile grow with its number.  All tiles of a query
+// head go to one XCD, whose L2 then holds that head's keys.
 #include <type_traits>
 
 #include "kv8.hpp"
@@ -10,6 +42,7 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
+// Excess of a scaled score over the reference that moves it: weights up to 2^6 cost no precision.
 constexpr float kPromptSlack = 6.0f;
 
 // Exponent of the weights' factor in a third pass: sums of up to 2^31 weights of up to
@@ -140,11 +173,8 @@ __device__ __forceinline__ void load_lds(const void *from, uint32_t at, uint32_t
 __device__ __forceinline__ void load_lds_wide(const void *from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(scalar((int)to)), "v"(from) : "memory");
 }
-// Waits until at most N of this wavefront's loads are under way (they end in order).
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
+// Waits for this wavefront's loads.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Source of the chunks that pad a K row.
 __device__ const uint4 kZeroChunk = {0, 0, 0, 0};
 
@@ -196,17 +226,18 @@ struct TileLoad {
     }
 };
 
-// LDS: ST tiles of K, ST of V.
-template <int DK, int DV, int KT, int ST>
-constexpr int prompt_lds() { return ST * KT * (DK + DV) * 2; }
+// LDS: two tiles of K, two of V.
+constexpr int kStages = 2;
+template <int DK, int DV, int KT>
+constexpr int prompt_lds() { return kStages * KT * (DK + DV) * 2; }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int ST, int EU>
+template <int DK, int DV, int NR, int WAVES, int KT, int EU>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))) void k_prompt(PromptArgs a) {
     constexpr int R = 32 * NR * WAVES;                // rows a workgroup
     constexpr int KB = KT / 32, DB = DV / 32;         // 32-token blocks, 32-dim blocks
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     constexpr int kTile = KT * DK * 2, vTile = KT * DV * 2;     // bytes
-    const uint32_t k_lds = lds_address(smem), v_lds = k_lds + ST * kTile;
+    const uint32_t k_lds = lds_address(smem), v_lds = k_lds + kStages * kTile;
     const int wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
 
     int head, item;
@@ -229,19 +260,19 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 
     const TileLoad<DK, KT, WAVES, false> lk(kbase, a.k.row, a.dk, wave, lane);
     const TileLoad<DV, KT, WAVES, true> lv(vbase, a.v.row, a.dv, wave, lane);
-    // Tile i lies in place i % ST.
+    // Tile i lies in place i % kStages.
     constexpr int kLoads = lk.N + lv.N;
     auto load = [&](int i) {
         const int t0 = keys.tile(i) * KT;
-        lk.load(k_lds + (i & (ST - 1)) * kTile, t0, n, wave);
-        lv.load(v_lds + (i & (ST - 1)) * vTile, t0, n, wave);
+        lk.load(k_lds + (i & (kStages - 1)) * kTile, t0, n, wave);
+        lv.load(v_lds + (i & (kStages - 1)) * vTile, t0, n, wave);
     };
     auto load_first = [&] {
         // (a zero that the compiler does not know: it would make the first tiles'
         // addresses once and keep them)
         const int first = scalar((int)opaque(0u));
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i)
+        for (int i = 0; i < kStages - 1; ++i)
             if (first + i < keys.count) load(first + i);
     };
     load_first();
@@ -315,14 +346,14 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
         l[r] = dot2(w[1], as_bf16x2(0x3F803F80u), l[r]);
     };
     // Scores of tile `it` less the reference, with the first reads of V and, where LOADS,
-    // tile `it` + ST - 1 on its way into LDS between the products.
+    // tile `it` + kStages - 1 on its way into LDS between the products.
     auto score = [&](auto loads, int it, auto read_v) {
         constexpr bool LOADS = decltype(loads)::value;
-        const int to = (it + ST - 1) & (ST - 1);
+        const int to = (it + kStages - 1) & (kStages - 1);
         const uint32_t k_to = k_lds + to * kTile, v_to = v_lds + to * vTile;
-        const int64_t t_to = LOADS ? keys.tile(it + ST - 1) * KT : 0;
+        const int64_t t_to = LOADS ? keys.tile(it + kStages - 1) * KT : 0;
         const uint16_t *k_from = lk.base + t_to * lk.stride, *v_from = lv.base + t_to * lv.stride;
-        const uint32_t at = opaque(k_at + (it & (ST - 1)) * kTile);
+        const uint32_t at = opaque(k_at + (it & (kStages - 1)) * kTile);
         bf16x8 kf[kAhead + 1][KB];
         auto read_k = [&](int c) {
             constexpr int W = DK % 128 ? 4 : 8;       // steps whose chunks the swizzle mixes
@@ -411,17 +442,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     };
     for (int it = scalar((int)opaque(0u)); it < keys.count; ++it) {
         const int t0 = keys.tile(it) * KT;
-        // up to ST - 2 later tiles may be on their way
-        const int later = keys.count - it - 1;
-        if (ST >= 4 && later >= 2) wait_loads<2 * kLoads>();
-        else if (ST >= 4 && later >= 1) wait_loads<kLoads>();
-        else wait_loads<0>();
+        wait_loads();
         __syncthreads();                              // and every wavefront is done with the tile before
-        const bool next = it + ST - 1 < keys.count, fast = next && t0 <= w_hi && lk.whole(keys.tile(it + ST - 1) * KT, n);
-        if (next && !fast) load(it + ST - 1);
+        const bool next = it + kStages - 1 < keys.count, fast = next && t0 <= w_hi && lk.whole(keys.tile(it + kStages - 1) * KT, n);
+        if (next && !fast) load(it + kStages - 1);
         if (slow && part(t0)) {                       // V without what is not finite (0 * NaN is NaN)
             for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
-                uint32_t &w = reinterpret_cast<uint32_t *>(smem + ST * kTile + (it & (ST - 1)) * vTile)[i];
+                uint32_t &w = reinterpret_cast<uint32_t *>(smem + kStages * kTile + (it & (kStages - 1)) * vTile)[i];
                 w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
             }
             __syncthreads();
@@ -430,7 +457,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
         // token 32 j + 16 e + 8 (i / 4) + 4 half + i % 4 is element i of the product's
         // operands: the order in which S comes out.  Fragment i: j, e, d = i / DB / 2,
         // i / DB % 2, i % DB.
-        const uint32_t vat = opaque(v_at + (it & (ST - 1)) * vTile);
+        const uint32_t vat = opaque(v_at + (it & (kStages - 1)) * vTile);
         auto read_v = [&](int i) {
             const int d = i % DB, e = i / DB % 2, j = i / DB / 2;
             union {
@@ -538,11 +565,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     }
 }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int ST, int EU>
+template <int DK, int DV, int NR, int WAVES, int KT, int EU>
 static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
     constexpr int R = 32 * NR * WAVES;
-    const size_t lds = prompt_lds<DK, DV, KT, ST>();
-    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, ST, EU>);
+    const size_t lds = prompt_lds<DK, DV, KT>();
+    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, EU>);
     if (int rc = allow_lds(fn, lds, who)) return rc;
     // sum over b of ceil(n_b / R)
     const int64_t most = a.max_rows < a.rows ? a.max_rows : a.rows;
@@ -551,7 +578,7 @@ static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
     if (other < items) items = other;
     const int64_t blocks = items * a.heads;
     if (!grid_fits(blocks, 64 * WAVES)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
-    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, ST, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
+    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
     return check_launch(who);
 }
 
@@ -609,9 +636,10 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     a.out_stride = out_row_stride;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int dk = q->dim, dv = v->dim;
-    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2, 2>(a, s, who);
-    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2, 2>(a, s, who);
-    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2, 2>(a, s, who);
-    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 2, 1>(a, s, who);
-    return launch_prompt<256, 256, 1, 4, 64, 2, 1>(a, s, who);
+    // the smallest tile that holds the dims; others are padded with zeros
+    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2>(a, s, who);
+    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2>(a, s, who);
+    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2>(a, s, who);
+    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 1>(a, s, who);
+    return launch_prompt<256, 256, 1, 4, 64, 1>(a, s, who);
 }
