@@ -24,8 +24,8 @@
 //    one's weights 1238 us there, but 64 more registers: packed prompts of 128 dims 506 us
 //    against 406).
 //  - 64-token tiles: 32-token ones with four stages spill or pay the barrier twice (128 dims:
-//    506 us).  Two workgroups a CU where the registers allow (dims up to 192 x 128: windowed
-//    prompts 465 -> 388 us); 192 x 192 and 256 x 256 have one wavefront a SIMD.
+//    506 us).  Two workgroups a CU where registers and LDS allow (dims up to 192 x 128: windowed
+//    prompts 465 us with one, 337 so); 192 x 192 and 256 x 256 have one wavefront a SIMD.
 //  - 24 prompts of up to 4500 rows, 32 + 8 heads of 128: 415 us, 857 TFLOP/s; 12001 rows of
 //    256 dims: 1337 us, 882 TFLOP/s (an 8192^3 product reaches 1222).  With everything but the
 //    products and barriers left out the latter takes 915 us.  What bounds it: one wavefront a
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     };
     auto mask = [&](int t0) {
         if (t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks)) return;
-        const int base = (int)opaque(t0 + 4 * half), window = a.window > 0 ? a.window : 0x7FFFFFFF, sink = a.sinks - base;
+        const int base = (int)opaque(t0 + 4 * half), window = a.window > 0 ? min(a.window, 0x7FFFF000) : 0x7FFFF000, sink = a.sinks - base;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int here = pos[r] - base, low = here - window;
@@ -560,7 +560,15 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     bool left = false;
 #pragma unroll
     for (int r = 0; r < NR; ++r) left |= !done[r];
-    if (!__syncthreads_or(left)) break;
+    // (__syncthreads_or would take static LDS, with which two 192 x 128 workgroups miss a CU)
+    int *flag = reinterpret_cast<int *>(smem);
+    __syncthreads();
+    if (threadIdx.x == 0) *flag = 0;
+    __syncthreads();
+    if (left) *flag = 1;
+    __syncthreads();
+    if (*flag == 0) break;
+    __syncthreads();
     load_first();
     }
 }
