@@ -763,7 +763,9 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
  * a cache, are kv8_attention's.
  *   q, k, v     [rows] head rows (e.g. parts of one q|k|v projection's rows): q's
  *               heads a multiple of k's and v's, q's dim k's; v may have another.
- *               Dims: multiples of 8 up to 256.
+ *               Dims: multiples of 8 up to 256 (64, 128, 192 with v's up to 128,
+ *               192 and 256 are the tiles; others are padded to the next).  k's and
+ *               v's row strides below 2^23.
  *   cu_rows     device int32 [batch + 1], 4-byte aligned.  Row ranges are cut to
  *               [0, rows).
  *   max_rows    host bound of a sequence's rows: those past it are not computed.
