@@ -157,22 +157,28 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     return v;
 }
 
+// (m0 among the clobbers is a reserved register, of which the compiler warns)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 // 16 bytes a lane from `from` + at[lane] to LDS address `to` + 16 * lane (from, to: the same
 // in every lane; lanes that are switched off load nothing).  In assembly, as the
 // compiler would wait for it before any later read of LDS; the caller waits
-// (wait_loads) before the barrier that hands the tile over.  m0 has no other user here.
+// (wait_loads) before the barrier that hands the tile over.  The compiler does not see the
+// load either, and the base is often the result of a v_readfirstlane just before: such a
+// register may be read as an address after five wait states (s_mov, s_nop 3), m0 after one.
 __device__ __forceinline__ void load_lds(const void *from, uint32_t at, uint32_t to) {
     const uint64_t f = reinterpret_cast<uint64_t>(from);
     const uint64_t base = (uint64_t)(uint32_t)scalar((int)(f >> 32)) << 32 | (uint32_t)scalar((int)f);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(scalar((int)to)), "v"(at), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 // ... from an address of each lane's own.
 __device__ __forceinline__ void load_lds_wide(const void *from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(scalar((int)to)), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(scalar((int)to)), "v"(from) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // Waits for this wavefront's loads.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Source of the chunks that pad a K row.
