@@ -359,11 +359,11 @@ __global__ __launch_bounds__(256) void k_moe_combine(const void *__restrict__ ys
     }
 }
 
-// One workgroup a token: dys rows w * dy, and dw = <ys row, dy>.
+// One workgroup a token: dys rows w * dy, and dw = <ys row, dy>.  dys may be ys.
 template <bool YS, bool Y, int K>
-__global__ __launch_bounds__(256) void k_moe_combine_grad(const void *__restrict__ dy, const void *__restrict__ ys, int m, int chunks,
+__global__ __launch_bounds__(256) void k_moe_combine_grad(const void *__restrict__ dy, const void *ys, int m, int chunks,
                                                           int top_k, const int32_t *__restrict__ place, const float *__restrict__ w,
-                                                          void *__restrict__ dys, float *__restrict__ dw) {
+                                                          void *dys, float *__restrict__ dw) {
     __shared__ float part[4][K];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t t = blockIdx.x;
