@@ -651,11 +651,15 @@ typedef struct nvfp4_kv8_pool {
  * Pages needed are ceil(kv_lens / page_tokens).  First the pages that a request holds
  * beyond them go back (their table entries become -1), the last request's last page
  * first; then the missing ones come from the top of the stack, the first request's
- * first page first, so that a step that is taken back leaves the stack as it was.  Where the
- * pool is empty the remaining entries become -1 (such tokens are not written and not
- * attended to), and the next call asks for them again.  Values that make no sense (lengths,
- * held, free_count below 0 or too large) are cut to their range.  One launch, or two
- * (many rows).
+ * first page first, so that a step that is taken back leaves the stack as it was.  Values that
+ * make no sense (lengths, held, free_count below 0 or too large) are cut to their range.  One
+ * launch, or two (many rows).
+ * Where the pool is empty the remaining entries become -1: this step's calls do not write
+ * such tokens and do not attend to them.  A request has gone short where kv_lens[b] >
+ * held[b] * page_tokens: its tokens from there on are not in the cache.  The next call's
+ * kept_lens[b] must be at most held[b] * page_tokens, and those tokens' rows are new ones again: a
+ * token that is kept without a page gets one by the next call, but with what its last owner
+ * left in it, and would be attended to.
  */
 int kv8_plan(const nvfp4_kv8_pool *pool, const int32_t *kept_lens, const int32_t *new_rows, int32_t rows,
              int32_t *cu_rows, int32_t *kv_lens, int32_t *positions, int64_t *slots, int32_t *missing, void *stream);

@@ -1012,6 +1012,13 @@ class KV8Pool:
         return KV8Pool(i32(batch, max_pages, fill=-1), i32(batch, fill=0),
                        torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device), i32(1, fill=num_pages), page_tokens)
 
+    def covered(self, lens: torch.Tensor) -> torch.Tensor:
+        """lens [batch] cut to the tokens that have a page, held * page_tokens: after a plan
+        that found the pool empty, what the next one may keep (the others are not in the
+        cache, and their rows are new ones again)."""
+        _vector(lens, torch.int32, self.batch, self.index, "lens")
+        return torch.minimum(lens, self.held * self.page_tokens)
+
 
 class KV8Plan(NamedTuple):
     """cu_rows [batch + 1] and kv_lens [batch]: with the pool's block_table the
@@ -1030,7 +1037,9 @@ def kv8_plan(pool: KV8Pool, kept_lens: torch.Tensor, new_rows: torch.Tensor, row
     """The next step's rows and pages: request b keeps kept_lens[b] tokens and
     gets new_rows[b] rows after them (int32 on the device; 0 and 0: it has
     ended); `rows` bounds all new rows.  Pages no longer needed go back to the
-    pool, missing ones come from it."""
+    pool, missing ones come from it.  kept_lens must not count tokens that an
+    earlier plan had no page for: where the pool may run empty, keep
+    pool.covered(lens)."""
     index, batch, i32 = pool.index, pool.batch, torch.int32
     _fits32(rows, "rows")
     if out is None:
