@@ -1,4 +1,5 @@
-"""kv8_plan where the pool runs dry, with the cache behind it."""
+"""kv8_plan where the pool runs dry, with the cache behind it, and without its row
+outputs."""
 import pytest
 import torch
 
@@ -54,3 +55,26 @@ def test_covered_cuts_to_the_pages_there_are(nvm):
     for bad in (i32([1, 2]), torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, dtype=torch.int32)):
         with pytest.raises(ValueError):
             pool.covered(bad)
+
+
+@pytest.mark.parametrize("rows", [900, 2048, 2049, 5000])
+@pytest.mark.parametrize("with_positions,with_slots", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("batch", [3, 1030])
+def test_without_row_outputs(nvm, rows, with_positions, with_slots, batch):
+    """No positions, no slots, neither: everything else as with them."""
+    pool, host = nvm.KV8Pool.empty(6000, batch, 200, 16), ref.Pool(6000, batch, 200, 16)
+    new = [rows // batch] * batch
+    new[0] += rows - sum(new)
+    kept = [(7 * b) % 40 for b in range(batch)]
+    at = torch.full((rows,), 9, dtype=torch.int32, device="cuda")
+    slots = torch.full((rows,), 9, dtype=torch.int64, device="cuda")
+    out = nvm.KV8Plan(i32([9] * (batch + 1)), i32([9] * batch), at if with_positions else None, slots if with_slots else None, i32([9]))
+    nvm.kv8_plan(pool, i32(kept), i32(new), rows, out=out)
+    want = host.plan(kept, new, rows)
+    if not with_positions:
+        assert at.tolist() == [9] * rows
+        at = i32(want[2])
+    if not with_slots:
+        assert slots.tolist() == [9] * rows
+        slots = torch.tensor(want[3], device="cuda")
+    compare(pool, host, out._replace(positions=at, slots=slots), want, rows)
