@@ -72,6 +72,13 @@ __device__ __forceinline__ int wave_sum(int v) {
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
+// ... of the two in a word.
+__device__ __forceinline__ bool any_not_finite(uint32_t two) { return not_finite(two) || not_finite(two >> 16); }
+// Two bf16 values, and to each the other word's where that is not finite.
+__device__ __forceinline__ uint32_t add_not_finite(uint32_t to, uint32_t v) {
+    const float lo = bf16_bits_to_f32(to & 0xFFFFu) + bf16_bits_to_f32(v & 0xFFFFu), hi = bf16_bits_to_f32(to >> 16) + bf16_bits_to_f32(v >> 16);
+    return (not_finite(v) ? f32_to_bf16_bits(lo) : to & 0xFFFFu) | (not_finite(v >> 16) ? f32_to_bf16_bits(hi) << 16 : to & 0xFFFF0000u);
+}
 
 // Rows of sequence b, cut to the call's bounds.
 __device__ __forceinline__ int2 prompt_rows(const PromptArgs &a, int b) {
@@ -409,10 +416,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 }
         }
     };
-    // whether some row of the workgroup does not see some token of a tile
-    auto part = [&](int t0) {
-        return t0 + KT - 1 > row0 || (a.window > 0 && t0 <= min(row0 + R, n) - 1 - a.window && t0 + KT > a.sinks);
-    };
     // Moves the reference to the row's maximum where scores exceed it by too much, or
     // where there is none yet.
     auto refer = [&] {
@@ -452,7 +455,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
         __syncthreads();                              // and every wavefront is done with the tile before
         const bool next = it + kStages - 1 < keys.count, fast = next && t0 <= w_hi && lk.whole(keys.tile(it + kStages - 1) * KT, n);
         if (next && !fast) load(it + kStages - 1);
-        if (slow && part(t0)) {                       // V without what is not finite (0 * NaN is NaN)
+        if (slow) {                                   // V without what is not finite (0 * NaN is NaN)
             for (int i = threadIdx.x; i < KT * DV / 2; i += 64 * WAVES) {
                 uint32_t &w = reinterpret_cast<uint32_t *>(smem + kStages * kTile + (it & (kStages - 1)) * vTile)[i];
                 w = (not_finite(w & 0xFFFFu) ? 0u : w & 0xFFFFu) | (not_finite(w >> 16) ? 0u : w & 0xFFFF0000u);
@@ -503,9 +506,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // A value that is not finite may come from a token that its row does not see, or from a
-    // sum past fp32's range: such rows once more without the former, in the tiles that some
-    // row sees in part, and if that does not help with smaller weights.  The others are done.
+    // A value that is not finite may come from a token that its row does not see, from one that
+    // it does (as infinity times a weight of 0, too), or from a sum past fp32's range: such rows
+    // once more without the former two, and if that does not help with smaller weights.  The
+    // others are done.
     bool write[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -518,31 +522,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
         const bool odd = !(__uint_as_float(sw.x) + __uint_as_float(sw.y) == 0.0f);      // (0 * NaN and 0 * inf are NaN)
         write[r] = !done[r] && (!odd || pass == 2);
         done[r] |= write[r];
-    }
-    if (slow) {
-        // the values that were left out, to the rows that see them
-        for (int it = 0; it < keys.count; ++it) {
-            const int t0 = keys.tile(it) * KT;
-            if (!part(t0)) continue;
-            for (int t = t0; t < min(t0 + KT, n); ++t) {
-                const uint16_t *vt = vbase + (int64_t)t * a.v.row;
-                bool bad = false;
-                for (int d = (int)opaque(lane); d < a.dv; d += 64) bad |= not_finite(vt[d]);
-                if (!__any(bad)) continue;
-                const uint16_t *vl = vt + opaque(4 * half);
-#pragma unroll
-                for (int d = 0; d < 4 * DB; ++d) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(vl + (8 * d < a.dv ? 8 * d : 0));
-                    const uint32_t w[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (not_finite(w[i]) && sees(t, pos[r])) o[r][d >> 2][4 * (d & 3) + i] += bf16_bits_to_f32(w[i]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-        }
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -562,6 +541,41 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 *reinterpret_cast<uint2 *>(dst + at) = make_uint2(f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16),
                                                                   f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16));
             }
+    }
+    if (slow) {
+        // The values that were left out, to the rows that see them, whatever their weights: in
+        // memory, where this lane has just written (the sums take all registers).
+        static_assert(KT == 64, "a token a lane");
+        for (int it = 0; it < keys.count; ++it) {
+            const int t0 = keys.tile(it) * KT;
+            if (t0 > w_hi) continue;
+            bool bad = false;
+            if (t0 + lane < n) {
+                const uint16_t *vt = vbase + (int64_t)(t0 + lane) * a.v.row;
+#pragma unroll 4
+                for (int d = 0; d < a.dv; d += 8) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vt + d);
+                    bad |= any_not_finite(v.x) | any_not_finite(v.y) | any_not_finite(v.z) | any_not_finite(v.w);
+                }
+            }
+            for (uint64_t odd = __ballot(bad); odd; odd &= odd - 1) {
+                const int t = t0 + __builtin_ctzll(odd);
+                const uint16_t *vt = vbase + (int64_t)t * a.v.row + 4 * half;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    if (!write[r] || !sees(t, pos[r])) continue;
+                    uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
+                    for (int d = 0; d < a.dv; d += 8) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(vt + d);
+                        if (!any_not_finite(v.x) && !any_not_finite(v.y)) continue;
+                        uint2 x = *reinterpret_cast<const uint2 *>(dst + d);
+                        x.x = add_not_finite(x.x, v.x);
+                        x.y = add_not_finite(x.y, v.y);
+                        *reinterpret_cast<uint2 *>(dst + d) = x;
+                    }
+                }
+            }
+        }
     }
     bool left = false;
 #pragma unroll
