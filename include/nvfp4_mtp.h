@@ -781,8 +781,10 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
  * Scores, softmax statistics and sums in fp32; weights are rounded to bf16 for the
  * product with v and for their sum.  What a row does not see never reaches it, NaN
  * and infinities included; a value of v that is not finite counts in every row that
- * sees it, however small its weight.  The result is the same on every call with the
- * same arguments.  One launch, no workspace.
+ * sees it, however small its weight.  Where q and k are finite,
+ * q k^T and its differences within a row have to be below 3.4e38; a row with a score of NaN
+ * or infinity, or none above -infinity, is NaN.  The result is the same on every call
+ * with the same arguments.  One launch, no workspace.
  */
 int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const nvfp4_head_rows *v,
                      const int32_t *cu_rows, int32_t batch, int32_t rows, int32_t max_rows, float scale,

@@ -526,7 +526,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
-        const float sum = __uint_as_float(sw.x) + __uint_as_float(sw.y), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float sum = __uint_as_float(sw.x) + __uint_as_float(sw.y), inv = 1.0f / sum;
+        // (a row sees itself: without a weight all its scores are -inf, and 0 * inf is NaN)
         if (!write[r]) continue;
         uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
 #pragma unroll

@@ -1,4 +1,4 @@
-"""prompt_attention where values or scores that a row sees are not finite."""
+"""prompt_attention where a value, or every score, that a row sees is not finite."""
 import math
 
 import pytest
@@ -66,6 +66,29 @@ def test_infinities_beside_sums_past_fp32(nvm, hq, hk, dk, dv):
     y = nvm.prompt_attention(q, k, v, cu_of([n]), n)
     other = [d for d in range(dv) if d != 2]
     assert bool((y[:, :, other] == top).all()) and bool((y[:7] == top).all()) and bool((y[7:, :, 2] == -math.inf).all())
+
+
+@pytest.mark.parametrize("hq,hk,dk,dv", DIMS)
+@pytest.mark.parametrize("how", ["k", "q", "range"])
+def test_rows_without_a_score_above_minus_infinity(nvm, hq, hk, dk, dv, how):
+    """No softmax: NaN.  Beside one finite score the others have no weight."""
+    n = 200
+    q, k, v = inputs(4, n, hq, hk, dk, dv)
+    q[:], k[:] = 0.0, 0.0
+    q[:, :, 0], k[:, :, 0] = 1.0, -1.0
+    if how == "k":
+        k[:, :, 0] = -math.inf
+    elif how == "q":
+        q[:, :, 0] = math.inf
+    else:
+        q[:, :, 0], k[:, :, 0] = 2.0 ** 70, -2.0 ** 70
+    y = nvm.prompt_attention(q, k, v, cu_of([n]), n)
+    assert bool(y.isnan().all())
+    if how != "q":
+        k[70, :, 0] = 0.0
+        y = nvm.prompt_attention(q, k, v, cu_of([n]), n)
+        want = v[70].repeat_interleave(hq // hk, 0)
+        assert bool(y[:70].isnan().all()) and bool((y[70:] == want).all())
 
 
 def test_a_score_of_infinity(nvm):
