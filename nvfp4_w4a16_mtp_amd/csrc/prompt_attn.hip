@@ -244,9 +244,9 @@ constexpr int kStages = 2;
 template <int DK, int DV, int KT>
 constexpr int prompt_lds() { return kStages * KT * (DK + DV) * 2; }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+template <int DK, int DV, int WAVES, int KT, int EU>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))) void k_prompt(PromptArgs a) {
-    constexpr int R = 32 * NR * WAVES;                // rows a workgroup
+    constexpr int R = 32 * WAVES;                     // rows a workgroup
     constexpr int KB = KT / 32, DB = DV / 32;         // 32-token blocks, 32-dim blocks
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     constexpr int kTile = KT * DK * 2, vTile = KT * DV * 2;     // bytes
@@ -290,30 +290,26 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     };
     load_first();
 
-    // the wavefront's rows: column blocks wave and 2 WAVES - 1 - wave of the tile
-    int pos[NR];
-    bf16x8 q[NR][DK / 16];
+    // the wavefront's rows: column block `wave` of the tile
+    const int pos = row0 + 32 * wave + col;
+    bf16x8 q[DK / 16];
+    const uint16_t *qrow = a.q.data + (int64_t)(r0 + min(pos, n - 1)) * a.q.row + (int64_t)head * a.q.head + 8 * half;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        pos[r] = row0 + 32 * (r == 0 ? wave : 2 * WAVES - 1 - wave) + col;
-        const uint16_t *p = a.q.data + (int64_t)(r0 + min(pos[r], n - 1)) * a.q.row + (int64_t)head * a.q.head + 8 * half;
+    for (int c = 0; c < DK / 16; ++c) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (16 * c + 8 * half < a.dk) w = *reinterpret_cast<const uint4 *>(qrow + 16 * c);
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        q[c] = __builtin_bit_cast(bf16x8, make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip));
+    }
+    if (a.zero) {                                     // (what is not finite stays: NaN)
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (16 * c + 8 * half < a.dk) w = *reinterpret_cast<const uint4 *>(p + 16 * c);
-            const uint32_t flip = a.negate ? 0x80008000u : 0u;
-            q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip));
-        }
-        if (a.zero) {                                 // (what is not finite stays: NaN)
-#pragma unroll
-            for (int c = 0; c < DK / 16; ++c) {
-                uint4 w = __builtin_bit_cast(uint4, q[r][c]);
-                auto only_odd = [](uint32_t x) { return (not_finite(x & 0xFFFFu) ? x & 0xFFFFu : 0u) | (not_finite(x >> 16) ? x & 0xFFFF0000u : 0u); };
-                q[r][c] = __builtin_bit_cast(bf16x8, make_uint4(only_odd(w.x), only_odd(w.y), only_odd(w.z), only_odd(w.w)));
-            }
+            uint4 w = __builtin_bit_cast(uint4, q[c]);
+            auto only_odd = [](uint32_t x) { return (not_finite(x & 0xFFFFu) ? x & 0xFFFFu : 0u) | (not_finite(x >> 16) ? x & 0xFFFF0000u : 0u); };
+            q[c] = __builtin_bit_cast(bf16x8, make_uint4(only_odd(w.x), only_odd(w.y), only_odd(w.z), only_odd(w.w)));
         }
     }
-    auto sees = [&](int t, int p) { return (t <= p) & ((a.window == 0) | (t > p - a.window) | (t < a.sinks)); };
+    auto sees = [&](int t) { return (t <= pos) & ((a.window == 0) | (t > pos - a.window) | (t < a.sinks)); };
 
     // The lane's place in a tile of K (row col, chunk half) and of V (row 4 half + lane
     // % 16 / 4, its 8 bytes of the group's 32): the swizzle makes other chunks and parts an exclusive
@@ -322,41 +318,36 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     const uint32_t k_at = k_lds + col * (2 * DK) + 16 * swizzle_k<DK>(half, col);
     const uint32_t v_at = v_lds + vrow * (2 * DV) + 16 * swizzle_v<DV>(2 * (col >> 4) + ((lane & 3) >> 1), vrow) + 8 * (lane & 1);
 
-    f32x16 o[NR][DB];
-    float m[NR], l[NR];                               // l: this lane's half of the tokens
-    f32x16 minus_m[NR];
-    bool done[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) done[r] = pos[r] >= n;
+    f32x16 o[DB];
+    float m, l;                                       // l: this lane's half of the tokens
+    f32x16 minus_m;
+    bool done = pos >= n;
 
     for (int pass = 0;; ++pass) {
     const bool slow = pass > 0;
+    m = l = 0.0f;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        m[r] = l[r] = 0.0f;
+    for (int i = 0; i < 16; ++i) minus_m[i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) minus_m[r][i] = 0.0f;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
-    }
-    const int w_lo = row0 + 32 * wave, w_hi = NR == 1 ? w_lo + 31 : row0 + 32 * (2 * WAVES - 1 - wave) + 31;
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    const int w_lo = row0 + 32 * wave, w_hi = w_lo + 31;
     constexpr int CS = DK / 16, kAhead = EU == 1 ? 3 : 2, kVAhead = EU == 1 ? 5 : 4;        // fragments read ahead of their products
     const float bias = pass > 1 ? -kLow : 0.0f;
-    f32x16 s[NR][KB];
-    bf16x8 p[NR][KB][2], vf[kVAhead + 1];
+    f32x16 s[KB];
+    bf16x8 p[KB][2], vf[kVAhead + 1];
     // four weights under the present reference, and their sum as rounded
-    auto weigh = [&](int r, int qd) {
+    auto weigh = [&](int qd) {
         const int j = qd / 4, g = qd % 4;
         bf16x2 w[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j][4 * g + i], a.scale, bias)));
-            p[r][j][g >> 1][4 * (g & 1) + i] = w[i >> 1][i & 1];
+            w[i >> 1][i & 1] = static_cast<__bf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[j][4 * g + i], a.scale, bias)));
+            p[j][g >> 1][4 * (g & 1) + i] = w[i >> 1][i & 1];
         }
-        l[r] = dot2(w[0], as_bf16x2(0x3F803F80u), l[r]);
-        l[r] = dot2(w[1], as_bf16x2(0x3F803F80u), l[r]);
+        l = dot2(w[0], as_bf16x2(0x3F803F80u), l);
+        l = dot2(w[1], as_bf16x2(0x3F803F80u), l);
     };
     // Scores of tile `it` less the reference, with the first reads of V and, where LOADS,
     // tile `it` + kStages - 1 on its way into LDS between the products.
@@ -395,59 +386,45 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             }
 #pragma unroll
             for (int j = 0; j < KB; ++j)
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    s[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[r][c], c == 0 ? minus_m[r] : s[r][j], 0, 0, 0);
+                s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % (kAhead + 1)][j], q[c], c == 0 ? minus_m : s[j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     auto mask = [&](int t0) {
         if (t0 + KT - 1 <= w_lo && (a.window == 0 || t0 > w_hi - a.window || t0 + KT <= a.sinks)) return;
         const int base = (int)opaque(t0 + 4 * half), window = a.window > 0 ? min(a.window, 0x7FFFF000) : 0x7FFFF000, sink = a.sinks - base;
+        const int here = pos - base, low = here - window;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const int here = pos[r] - base, low = here - window;
+        for (int j = 0; j < KB; ++j)
 #pragma unroll
-            for (int j = 0; j < KB; ++j)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 32 * j + 8 * (i >> 2) + (i & 3);     // the token less base
-                    s[r][j][i] = (t <= here) & ((t > low) | (t < sink)) ? s[r][j][i] : -INFINITY;
-                }
-        }
+            for (int i = 0; i < 16; ++i) {
+                const int t = 32 * j + 8 * (i >> 2) + (i & 3);     // the token less base
+                s[j][i] = (t <= here) & ((t > low) | (t < sink)) ? s[j][i] : -INFINITY;
+            }
     };
     // Moves the reference to the row's maximum where scores exceed it by too much, or
     // where there is none yet.
     auto refer = [&] {
-        float mx[NR];
-        bool need = false;
+        float mx = s[0][0];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            mx[r] = s[r][0][0];
+        for (int i = 1; i < 16 * KB; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
+        u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+        mx = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
+        if (!__any(mx * a.scale > kPromptSlack || l == 0.0f)) return;
+        // (a half may hold no weight yet: the row has one if either does)
+        sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+        const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
+        // (a row that needs no move stays as it is, whatever its neighbours do)
+        const float up = mx * a.scale > kPromptSlack || (fresh && mx > -INFINITY) ? mx : 0.0f;
+        const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
+        m += up;
+        l *= alpha;
 #pragma unroll
-            for (int i = 1; i < 16 * KB; ++i) mx[r] = fmaxf(mx[r], s[r][i >> 4][i & 15]);
-            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx[r]), __float_as_uint(mx[r]), false, false);
-            mx[r] = fmaxf(__uint_as_float(sw.x), __uint_as_float(sw.y));
-            need |= mx[r] * a.scale > kPromptSlack || l[r] == 0.0f;
-        }
-        if (!__any(need)) return;
+        for (int d = 0; d < DB; ++d) o[d] *= alpha;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            // (a half may hold no weight yet: the row has one if either does)
-            const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
-            const bool fresh = __uint_as_float(sw.x) == 0.0f && __uint_as_float(sw.y) == 0.0f;
-            // (a row that needs no move stays as it is, whatever its neighbours do)
-            const float up = mx[r] * a.scale > kPromptSlack || (fresh && mx[r] > -INFINITY) ? mx[r] : 0.0f;
-            const float alpha = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale);
-            m[r] += up;
-            l[r] *= alpha;
+        for (int j = 0; j < KB; ++j) s[j] -= up;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) o[r][d] *= alpha;
-#pragma unroll
-            for (int j = 0; j < KB; ++j) s[r][j] -= up;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) minus_m[r][i] = -m[r];
-        }
+        for (int i = 0; i < 16; ++i) minus_m[i] = -m;
     };
     for (int it = scalar((int)opaque(0u)); it < keys.count; ++it) {
         const int t0 = keys.tile(it) * KT;
@@ -487,9 +464,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
         // The weights of 16 tokens beside the products of the 16 before: exponentials on the
         // vector units while the matrix cores are busy.
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int qd = 0; qd < 2; ++qd) weigh(r, qd);
+        for (int qd = 0; qd < 2; ++qd) weigh(qd);
         __builtin_amdgcn_sched_barrier(0);
         constexpr int PS = 2 * KB * DB;
 #pragma unroll
@@ -497,11 +472,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
             if (i + kVAhead < PS) read_v(i + kVAhead);
             __builtin_amdgcn_sched_barrier(0);
             const int group = i / DB, d = i % DB;
-#pragma unroll
-            for (int r = 0; r < NR; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[r][group / 2][group % 2], o[r][d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % (kVAhead + 1)], p[group / 2][group % 2], o[d], 0, 0, 0);
             if (group + 1 < 2 * KB) {
 #pragma unroll
-                for (int z = d * 2 * NR / DB; z < (d + 1) * 2 * NR / DB; ++z) weigh(z / 2, 2 * (group + 1) + z % 2);
+                for (int z = d * 2 / DB; z < (d + 1) * 2 / DB; ++z) weigh(2 * (group + 1) + z);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -510,26 +484,20 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     // it does (as infinity times a weight of 0, too), or from a sum past fp32's range: such rows
     // once more without the former two, and if that does not help with smaller weights.  The
     // others are done.
-    bool write[NR];
+    float far = 0.0f;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        float far = 0.0f;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) far = __builtin_fmaf(o[r][d][i], 0.0f, far);
-        const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(far), __float_as_uint(far), false, false);
-        const bool odd = !(__uint_as_float(sw.x) + __uint_as_float(sw.y) == 0.0f);      // (0 * NaN and 0 * inf are NaN)
-        write[r] = !done[r] && (!odd || pass == 2);
-        done[r] |= write[r];
-    }
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[r]), __float_as_uint(l[r]), false, false);
-        const float sum = __uint_as_float(sw.x) + __uint_as_float(sw.y), inv = 1.0f / sum;
-        // (a row sees itself: without a weight all its scores are -inf, and 0 * inf is NaN)
-        if (!write[r]) continue;
-        uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
+        for (int i = 0; i < 16; ++i) far = __builtin_fmaf(o[d][i], 0.0f, far);
+    u32x2 sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(far), __float_as_uint(far), false, false);
+    const bool odd = !(__uint_as_float(sw.x) + __uint_as_float(sw.y) == 0.0f);      // (0 * NaN and 0 * inf are NaN)
+    const bool write = !done && (!odd || pass == 2);
+    done |= write;
+    sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    // (a row sees itself: without a weight all its scores are -inf, and 0 * inf is NaN)
+    const float inv = 1.0f / (__uint_as_float(sw.x) + __uint_as_float(sw.y));
+    uint16_t *dst = a.out + (int64_t)(r0 + pos) * a.out_stride + (int64_t)head * a.dv + 4 * half;
+    if (write) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -538,7 +506,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
                 if (at >= a.dv) continue;
                 float x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = o[r][d][4 * g + i] * inv;
+                for (int i = 0; i < 4; ++i) x[i] = o[d][4 * g + i] * inv;
                 *reinterpret_cast<uint2 *>(dst + at) = make_uint2(f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16),
                                                                   f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16));
             }
@@ -556,37 +524,30 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
 #pragma unroll 4
                 for (int d = 0; d < a.dv; d += 8) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(vt + d);
-                    bad |= any_not_finite(v.x) | any_not_finite(v.y) | any_not_finite(v.z) | any_not_finite(v.w);
+                    bad = bad || any_not_finite(v.x) || any_not_finite(v.y) || any_not_finite(v.z) || any_not_finite(v.w);
                 }
             }
-            for (uint64_t odd = __ballot(bad); odd; odd &= odd - 1) {
-                const int t = t0 + __builtin_ctzll(odd);
+            for (uint64_t tokens = __ballot(bad); tokens; tokens &= tokens - 1) {
+                const int t = t0 + __builtin_ctzll(tokens);
                 const uint16_t *vt = vbase + (int64_t)t * a.v.row + 4 * half;
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    if (!write[r] || !sees(t, pos[r])) continue;
-                    uint16_t *dst = a.out + (int64_t)(r0 + pos[r]) * a.out_stride + (int64_t)head * a.dv + 4 * half;
-                    for (int d = 0; d < a.dv; d += 8) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vt + d);
-                        if (!any_not_finite(v.x) && !any_not_finite(v.y)) continue;
-                        uint2 x = *reinterpret_cast<const uint2 *>(dst + d);
-                        x.x = add_not_finite(x.x, v.x);
-                        x.y = add_not_finite(x.y, v.y);
-                        *reinterpret_cast<uint2 *>(dst + d) = x;
-                    }
+                if (!write || !sees(t)) continue;
+                for (int d = 0; d < a.dv; d += 8) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vt + d);
+                    if (!any_not_finite(v.x) && !any_not_finite(v.y)) continue;
+                    uint2 x = *reinterpret_cast<const uint2 *>(dst + d);
+                    x.x = add_not_finite(x.x, v.x);
+                    x.y = add_not_finite(x.y, v.y);
+                    *reinterpret_cast<uint2 *>(dst + d) = x;
                 }
             }
         }
     }
-    bool left = false;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) left |= !done[r];
     // (__syncthreads_or would take static LDS, with which two 192 x 128 workgroups miss a CU)
     int *flag = reinterpret_cast<int *>(smem);
     __syncthreads();
     if (threadIdx.x == 0) *flag = 0;
     __syncthreads();
-    if (left) *flag = 1;
+    if (!done) *flag = 1;
     __syncthreads();
     if (*flag == 0) break;
     __syncthreads();
@@ -594,11 +555,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(EU))
     }
 }
 
-template <int DK, int DV, int NR, int WAVES, int KT, int EU>
+template <int DK, int DV, int WAVES, int KT, int EU>
 static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
-    constexpr int R = 32 * NR * WAVES;
+    constexpr int R = 32 * WAVES;
     const size_t lds = prompt_lds<DK, DV, KT>();
-    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, NR, WAVES, KT, EU>);
+    const void *fn = reinterpret_cast<const void *>(k_prompt<DK, DV, WAVES, KT, EU>);
     if (int rc = allow_lds(fn, lds, who)) return rc;
     // sum over b of ceil(n_b / R)
     const int64_t most = a.max_rows < a.rows ? a.max_rows : a.rows;
@@ -607,7 +568,7 @@ static int launch_prompt(const PromptArgs &a, hipStream_t s, const char *who) {
     if (other < items) items = other;
     const int64_t blocks = items * a.heads;
     if (!grid_fits(blocks, 64 * WAVES)) return fail(NVFP4_ERR_UNSUPPORTED, "%s: grid too large", who);
-    hipLaunchKernelGGL((k_prompt<DK, DV, NR, WAVES, KT, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
+    hipLaunchKernelGGL((k_prompt<DK, DV, WAVES, KT, EU>), dim3((unsigned)blocks), dim3(64 * WAVES), lds, s, a);
     return check_launch(who);
 }
 
@@ -666,9 +627,9 @@ extern "C" int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows 
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int dk = q->dim, dv = v->dim;
     // the smallest tile that holds the dims; others are padded with zeros
-    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 1, 4, 64, 2>(a, s, who);
-    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 1, 4, 64, 2>(a, s, who);
-    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 1, 4, 64, 2>(a, s, who);
-    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 1, 4, 64, 1>(a, s, who);
-    return launch_prompt<256, 256, 1, 4, 64, 1>(a, s, who);
+    if (dk <= 64 && dv <= 64) return launch_prompt<64, 64, 4, 64, 2>(a, s, who);
+    if (dk <= 128 && dv <= 128) return launch_prompt<128, 128, 4, 64, 2>(a, s, who);
+    if (dk <= 192 && dv <= 128) return launch_prompt<192, 128, 4, 64, 2>(a, s, who);
+    if (dk <= 192 && dv <= 192) return launch_prompt<192, 192, 4, 64, 1>(a, s, who);
+    return launch_prompt<256, 256, 4, 64, 1>(a, s, who);
 }
