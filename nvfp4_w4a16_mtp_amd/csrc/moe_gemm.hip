@@ -287,11 +287,16 @@ static MoeGemmLayout moe_gemm_layout(int m, int top_k, const nvfp4_moe_weights *
     MoeGemmLayout l;
     const int64_t pairs = (int64_t)m * top_k, E = e->num_experts;
     const int64_t avg = pairs / E;
-    // Tiles that hold the average expert's rows with some to spare: a tile costs its weights
-    // once however few rows it has, and a row past the last tile another one.  (40 rows of top-8
-    // of 256, 1.25 rows an expert: 16-row tiles of k_moe_rows 57 us for gate and up, of
-    // k_moe_gemm 104; 4096 rows, 128 an expert: 128-row tiles 268, 64-row ones 314.)
-    l.bm = avg <= 12 ? 16 : avg <= 24 ? 32 : avg <= 48 ? 64 : kMoeBM;
+    // A tile costs its weights once however few rows it has, and a row past the last tile
+    // another one.  The whole call at top-8 of 256, hidden 2048, with tiles of 16, 32 and 128
+    // rows, us (rows an expert: inter 512; inter 1024):
+    //     1: 106 121 150; 196 215 277       8: 161 184 228; 279 307 414
+    //    12: 173 189 233; 303 314 422      16: 204 194 238; 360 321 433
+    //    32: 311 265 265; 581 456 472      48: 419 352 295; 777 596 530
+    //   128: 970 752 505; 1821 1287 838
+    // (k_moe_rows with 64 rows, one wavefront a SIMD, lost to one of them everywhere: 32 rows
+    // an expert 358 and 633, 48 407 and 702.)
+    l.bm = avg <= 12 ? 16 : avg <= 32 ? 32 : kMoeBM;
     // sum over the experts of ceil(n_e / bm)
     l.max_tiles = pairs / l.bm + (pairs < E ? pairs : E);
     size_t at = 0;
@@ -317,7 +322,6 @@ static void launch_moe_gemm(int bm, int64_t blocks, const MoeGemmArgs &a, hipStr
     const dim3 g((unsigned)blocks), b(256);
     if (bm == 16) hipLaunchKernelGGL((k_moe_rows<1, GATE_UP>), g, b, 0, s, a);
     else if (bm == 32) hipLaunchKernelGGL((k_moe_rows<2, GATE_UP>), g, b, 0, s, a);
-    else if (bm == 64) hipLaunchKernelGGL((k_moe_rows<4, GATE_UP>), g, b, 0, s, a);
     else hipLaunchKernelGGL((k_moe_gemm<GATE_UP>), g, b, 0, s, a);
 }
 
