@@ -21,7 +21,7 @@ struct SortArgs {
     float *w;                // [m][top_k]
     int32_t *offsets;        // [experts + 1]
     int32_t *order, *place;  // [m * top_k]
-    int32_t *hist;           // [blocks][experts]
+    int32_t *hist;           // [blocks][(experts + 1) / 2], two experts a word
     int per_block;           // tokens a block of the counting launch
     MoeTile *tiles;          // NULL, or the tile map
     int32_t *tile_count;     // [1], with tiles

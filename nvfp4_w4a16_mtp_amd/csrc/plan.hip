@@ -5,10 +5,12 @@
 // passes: prefix sums of the new rows (cu_rows, lengths); pages that go, pushed on the
 // stack of free pages; pages that come, popped from it.  A chunk's pages are spread
 // over all threads: page i belongs to the request whose prefix sums enclose it, found
-// by bisection in LDS.  Nothing but latency: a decode step moves a few KB, through a
-// chain of loads, scans and barriers.  Few rows' positions and slots are written here,
-// many by a second launch.  64 requests: 8 us a launch; 700 with 70 k rows of prompts: 25 us,
-// and 5 us for the rows.
+// by bisection in LDS.  A decode step is all latency: a few KB, through a chain of loads,
+// scans and barriers.  Few rows' positions and slots are written here,
+// many by a second launch.  64 requests that give back 1530 pages: 8 us a launch.  700 with
+// 166 k rows of prompts that give back 19.6 k pages and take 2.6 k: 25 us, the throughput of one
+// CU (a round of 1024 pages costs a bisection and a chain of scattered loads and stores), and
+// 5 us for the rows.
 #include "common.hpp"
 
 namespace nvfp4 {
@@ -210,8 +212,15 @@ __global__ __launch_bounds__(256) void k_plan_rows(PlanArgs a) {
     write_row(a, lo, a.lens[lo] - a.cu[lo + 1], r, r);
 }
 
-// Rows written by the planning workgroup itself: two a thread, less than another launch.
+// Rows written by the planning workgroup itself, without another launch: 64 requests, 2048
+// rows 6.6 us a call (8.0 with the launch), 4096 rows 8.0 (7.9); 700 requests 7.4 (9.2) and 9.2
+// (9.2).
 constexpr int kRowsHere = 2048;
+
+// Threads of the planning workgroup.  Fewer wavefronts pass their barriers sooner, more walk the
+// requests and rows in fewer steps: 64 requests, 512 rows 5.1 us with 256 threads (5.8 with
+// 1024), 1024 rows 6.3 (5.9); 200 requests, 800 rows 6.8 (6.0).
+static int plan_threads(int batch, int rows) { return batch <= 64 && rows <= 512 ? 256 : kPlanThreads; }
 
 }  // namespace nvfp4
 
@@ -239,7 +248,7 @@ extern "C" int kv8_plan(const nvfp4_kv8_pool *pool, const int32_t *kept_lens, co
                __builtin_ctz((unsigned)p), kept_lens, new_rows, rows, cu_rows, kv_lens, positions, slots, missing};
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool write = rows > 0 && pool->batch > 0 && (positions || slots), here = write && rows <= kRowsHere;
-    hipLaunchKernelGGL(k_plan, dim3(1), dim3(pool->batch <= 256 && rows <= 1024 ? 256 : kPlanThreads), 0, s, a, here ? 1 : 0);
+    hipLaunchKernelGGL(k_plan, dim3(1), dim3(plan_threads(pool->batch, rows)), 0, s, a, here ? 1 : 0);
     if (write && !here) hipLaunchKernelGGL(k_plan_rows, dim3((unsigned)(((int64_t)rows + 255) / 256)), dim3(256), 0, s, a);
     return check_launch(who);
 }
