@@ -490,8 +490,8 @@ int moe_sort(const float *router_logits, int32_t m, int32_t num_experts, int32_t
  *              16-byte aligned; hidden % 8 == 0.
  *   place      as moe_sort; pairs whose place is outside [0, m * top_k) are passed
  *              over, here and in the calls below.
- *   out        [m * top_k][hidden] of x's type, 16-byte aligned; rows of no pair are
- *              left as they were.
+ *   out        [m * top_k][hidden] of x's type, 16-byte aligned, must not overlap x;
+ *              rows of no pair are left as they were.
  * Its gradient is moe_combine without weights.  One launch.
  */
 int moe_gather(const void *x, int32_t x_dtype, int32_t m, int32_t hidden, int32_t top_k, const int32_t *place, void *out,
@@ -501,7 +501,7 @@ int moe_gather(const void *x, int32_t x_dtype, int32_t m, int32_t hidden, int32_
  * moe_combine -- sorted rows back to their tokens, with the weights applied:
  * y[t] = sum over j, in slot order, of topk_w[t][j] * ys[place[t][j]], fp32 sums.
  *   ys, y      [m * top_k][hidden] and [m][hidden], fp32 or bf16 each, 16-byte aligned;
- *              hidden % 8 == 0.  A token without rows becomes zero.
+ *              hidden % 8 == 0; they must not overlap.  A token without rows becomes zero.
  *   topk_w     [m][top_k] fp32, or NULL: weights of 1.
  * One launch.
  */
@@ -781,10 +781,11 @@ int kv8_attention(const nvfp4_head_rows *q, const nvfp4_kv8_cache *cache, const 
  * Scores, softmax statistics and sums in fp32; weights are rounded to bf16 for the
  * product with v and for their sum.  What a row does not see never reaches it, NaN
  * and infinities included; a value of v that is not finite counts in every row that
- * sees it, however small its weight.  Where q and k are finite,
- * q k^T and its differences within a row have to be below 3.4e38; a row with a score of NaN
- * or infinity, or none above -infinity, is NaN.  The result is the same on every call
- * with the same arguments.  One launch, no workspace.
+ * sees it, however small its weight.  An average of finite values is finite; where a
+ * row's sum before the division passes 3.4e38, terms below 2^-86 may be lost.  Where q and
+ * k are finite, q k^T and its differences within a row have to be below 3.4e38; a row with a
+ * score of NaN or infinity, or none above -infinity, is NaN.  The result is the same on
+ * every call with the same arguments.  One launch, no workspace.
  */
 int prompt_attention(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const nvfp4_head_rows *v,
                      const int32_t *cu_rows, int32_t batch, int32_t rows, int32_t max_rows, float scale,

@@ -36,8 +36,8 @@ struct MoeGemmArgs {
 
 // One row tile (128 rows of one expert) by 128 weight rows, dequantized on the way into LDS
 // as in the prompt GEMM, whose 128-row rate it reaches (4096 rows of top-8 of 256 experts:
-// 393 tiles, 65% full, gate and up 268 us, 787 TFLOP/s counting whole tiles).  Measured
-// against it there: 64-row tiles 314 us, 256-row tiles 359, 128-k steps 314, four
+// 393 tiles, 65% full, gate and up 291 us on average and 268 at least, 725 and 787 TFLOP/s
+// counting whole tiles).  Measured against the latter there: 64-row tiles 314 us, 256-row tiles 359, 128-k steps 314, four
 // wavefronts a SIMD 392 (they spill), the weights of four steps asked for at once 294, a row
 // tile's columns on one XCD 268.  GATE_UP: 64 rows of
 // gate and the same 64 of up, in turn by 16, so that a wavefront has both of an output.

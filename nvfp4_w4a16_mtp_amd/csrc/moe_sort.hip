@@ -6,9 +6,9 @@
 // within a block from ballots, so that the order does not depend on timing.  8191 tokens of
 // 256 experts, top-8: 11 us to route and count (bound by the selections' instructions: some 600
 // a token), 8 us to place.  Blocks of 16 tokens: 12 and 11 us, of 64: 17 and 7.
-// Rows out, back and the gradient move every byte once, at 5.2 to 5.9 TB/s (a large copy
-// reaches 5.1): 8191 tokens of 2048 to eight places 51 us and back 57 us; the gradient of
-// 2000 tokens of 7168, 96-104 us.
+// Rows out, back and the gradient move every byte once (a large copy reaches 5.1 TB/s): 8191
+// tokens of 2048 to eight places 51 us, 5.9 TB/s, and back 57 us, 5.2; the gradient of 2000
+// tokens of 7168, 104 us, 4.7.
 #include "moe_sort.hpp"
 
 namespace nvfp4 {

@@ -14,22 +14,24 @@
 // A lane's column is a row of queries in both products, and S^T comes out of the first in
 // a lane order that is the second's operand order up to a permutation of the tokens; V is
 // read in the same permutation (transposing LDS reads), so P never leaves its registers.
-// Tiles go from memory straight into LDS (double buffered, swizzled at the source so that no
-// read has a bank conflict: none counted), each fragment is read a few products ahead.
+// Tiles go from memory straight into LDS (double buffered, swizzled at the source so that
+// reads have few bank conflicts: none counted at 128 and 256 dims, 37% of the LDS cycles at 192,
+// where the swizzle has eight places), each fragment is read a few products ahead.
 //  - The first product accumulates onto -m, so a weight is one multiplication and 2^x, and the
 //    reference moves only where a row's score exceeds it by kPromptSlack (2^6 in the weights).
 //  - The weights of 16 tokens are made beside the products of the 16 before: exponentials run
 //    on the vector units while the matrix cores are busy (12001 rows, 16 + 2 heads of 256:
-//    2257 us with no read-ahead, 1552 with it, 1337 so; the next tile's scores beside this
+//    2257 us with no read-ahead, 1552 with it, 1323 so; the next tile's scores beside this
 //    one's weights 1238 us there, but 64 more registers: packed prompts of 128 dims 506 us
-//    against 406).
+//    against 404).
 //  - 64-token tiles: 32-token ones with four stages spill or pay the barrier twice (128 dims:
 //    506 us).  Two workgroups a CU where registers and LDS allow (dims up to 192 x 128: windowed
-//    prompts 465 us with one, 337 so); 192 x 192 and 256 x 256 have one wavefront a SIMD.
-//  - 24 prompts of up to 4500 rows, 32 + 8 heads of 128: 415 us, 857 TFLOP/s; 12001 rows of
-//    256 dims: 1337 us, 882 TFLOP/s (an 8192^3 product reaches 1222).  With everything but the
+//    prompts 465 us with one, 325 so); 192 x 192 and 256 x 256 have one wavefront a SIMD.
+//  - 24 prompts of up to 4500 rows, 32 + 8 heads of 128: 404 us, 880 TFLOP/s; 12001 rows of
+//    256 dims: 1323 us, 893 TFLOP/s (an 8192^3 product reaches 1222).  With everything but the
 //    products and barriers left out the latter takes 915 us.  What bounds it: one wavefront a
-//    SIMD with little to cover the waits between its two products.
+//    SIMD with little to cover the waits between its two products (matrix cores busy 38%); at
+//    128 dims matrix cores busy 47%, vector issue 51%.
 // Long prompts' tiles first: the keys of a row tile grow with its number.  All tiles of a query
 // head go to one XCD, whose L2 then holds that head's keys.
 #include <type_traits>
